@@ -147,6 +147,80 @@ struct FwdParams {
   long long* trace;             // development timing probe; always null in the library
 };
 
+// Rotary embedding of strided q and k (t = 0, 1).  Strides in elements, over
+// (batch entry, token, head).
+struct RotaryParams {
+  const void* x[2];
+  void* y[2];
+  int H[2];                     // heads; 0 = tensor absent
+  int64_t xs[2][3], ys[2][3];
+  int B, S, d, parts, rot;      // each of the `parts` equal parts of a head turns its first rot channels
+  const int32_t* pos;           // [B or 1][S][n_axes]
+  int64_t pos_stride_b;
+  int n_axes;
+  int axis_end[3];              // pairs below axis_end[0] turn by axis 0, below axis_end[1] by axis 1, ...
+  const double* freqs;          // [rot / 2]
+  float scale;                  // factor of the rotated channels
+  int inverse;
+  long long tokens;             // B * S
+  int units, per, shares;       // set by the launcher
+};
+cudaError_t launch_rotary(const RotaryParams& p, int dtype, bool half, cudaStream_t st);
+
+// Linear layer y = act(x w^T + bias) + residual.
+struct LinearPlan {
+  bool pair;                    // 256 x 256 tiles by CTA pairs
+  bool swap;                    // few rows: W's rows are the MMA's rows
+  int bn, splits;               // of the one-CTA tiles
+};
+struct LinearParams {
+  int M, N, K;
+  const uint16_t *x, *w;
+  int64_t ldx, ldw, ldy, ldr;
+  const void* bias;             // [N] or null
+  const void* residual;         // [M][N] of out_dtype, or null
+  void* y;
+  int in_bf16, out_dtype, bias_dtype, act;
+  uint32_t* status;
+  uint64_t timeout_ns;
+  // set by the launcher: the tile kernels' operands in their MMA roles
+  const uint16_t *a, *b;
+  int64_t lda, ldb, rows_a, rows_b;
+  int tiles_a, tiles_b, splits;
+  int vec_y, vec_r;             // bytes of the widest aligned access of y's and residual's rows, 0 = elements
+};
+LinearPlan plan_linear(int M, int N, int K, bool tma);
+// tx, tw: 2-D maps with 64-element boxes of plan.pair ? 128 : (swap ? bn : 128) rows of x and
+// plan.pair ? 128 : (swap ? 128 : bn) rows of w; unused without tma.
+cudaError_t launch_linear(LinearParams p, const LinearPlan& plan, bool tma, const CUtensorMap& tx,
+                          const CUtensorMap& tw, cudaStream_t st);
+
+// Differential attention.  n_groups row ranges per batch entry: H_kv ranges
+// of the packed rows (head, query) of the heads that share a K/V head, or H
+// ranges of one head's queries.
+struct DiffParams {
+  int B, H, H_kv, S_q, S_kv;
+  int n_groups, hpg, R, n_rt;   // heads and rows of a range, its 128-row tiles
+  int splits;                   // parts the keys are walked in (workspace when > 1)
+  float scale_log2;
+  const float* lam;             // [4][H][d / 2]
+  float lambda_init;
+  const float* norm_w;          // [d] or null
+  float eps;
+  const int32_t* kv_len;        // [B] or null
+  const uint8_t* key_mask;      // [B][S_kv], nonzero = takes part, or null
+  __nv_bfloat16* o;             // [B][S_q][H][d]
+  float* lse;                   // [2][B][H][S_q] or null
+  float* part_o;                // [splits][2][B*H*S_q][d]
+  float* part_l;                // [splits][2][B*H*S_q], log2 units
+  uint32_t* status;
+  uint64_t timeout_ns;
+};
+int diff_splits(long long items, int S_kv);
+// The maps describe (d, rows, heads or ranges, batch) with boxes of 64 x 128.
+cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
+                             const CUtensorMap& tv, cudaStream_t st);
+
 // out_kind: 0 = fp16, 1 = bf16, 2 = e4m3
 cudaError_t launch_rope_qkv(const RopeParams& p, int out_kind, cudaStream_t st);
 cudaError_t launch_quant_fp8(const QuantParams& p, bool in_bf16, cudaStream_t st);
@@ -166,6 +240,14 @@ cudaError_t launch_fwd_f16_hp(const FwdParams& p, int d, const CUtensorMap& tq, 
 
 // Rows of the K / V tiles the forward kernels walk (the TMA box height).
 int fwd_kv_rows();
+
+// The current device's status word (null on error) and multiprocessor count.
+uint32_t* device_status_ptr();
+int device_sm_count();
+// cuTensorMapEncodeTiled of `rank` dimensions of 16-bit elements (128-byte
+// swizzle, zeros out of bounds); false on error.  strides in bytes, rank - 1.
+bool encode_map16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides,
+                  const uint32_t* box);
 
 cudaError_t launch_selftest_wait(uint32_t* status, uint64_t limit_ns, cudaStream_t st);
 

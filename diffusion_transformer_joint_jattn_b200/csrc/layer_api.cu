@@ -1,0 +1,276 @@
+// C-ABI entry points of the layer around the attention (rotary embedding,
+// linear layer, differential attention): argument validation before any
+// launch, tensor maps, launches on the caller's stream.
+#include <cmath>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "jattn.h"
+#include "jattn_internal.h"
+
+namespace {
+
+constexpr uint64_t kTimeoutNs = 2000000000ull;   // 2 s per pipeline wait
+
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+int elem_bytes(jattn_dtype t) { return t == JATTN_FP32 ? 4 : 2; }
+bool is_16bit(jattn_dtype t) { return t == JATTN_BF16 || t == JATTN_FP16; }
+bool is_float(jattn_dtype t) { return is_16bit(t) || t == JATTN_FP32; }
+
+jattn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? JATTN_OK : JATTN_ERR_CUDA; }
+
+// 2-D map of a [rows][cols] 16-bit matrix, boxes of 64 columns x box_rows.
+bool matrix_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(rows > 1 ? ld : (cols + 7) / 8 * 8) * 2};
+  const uint32_t box[2] = {64u, static_cast<uint32_t>(box_rows)};
+  return jattn::encode_map16(m, base, 2, dims, strides, box);
+}
+
+// (d, rows, heads, batch) map of 16-bit elements, boxes of 64 channels x 128
+// rows; a dimension of one element gets a harmless stride.
+bool heads_map(CUtensorMap* m, const void* base, int d, int64_t rows, int64_t heads, int64_t batch, int64_t row_stride,
+               int64_t head_stride, int64_t batch_stride) {
+  const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(heads),
+                            static_cast<uint64_t>(batch)};
+  const uint64_t strides[3] = {static_cast<uint64_t>(rows > 1 ? row_stride : d) * 2,
+                               static_cast<uint64_t>(heads > 1 ? head_stride : d) * 2,
+                               static_cast<uint64_t>(batch > 1 ? batch_stride : d) * 2};
+  const uint32_t box[4] = {64u, 128u, 1u, 1u};
+  return jattn::encode_map16(m, base, 4, dims, strides, box);
+}
+
+// Row ranges of a call: the rows of the heads that share a K/V head form one
+// range when they are equally spaced in memory.
+struct DiffRanges {
+  int n_groups, hpg, R, n_rt, splits;
+  int64_t row_stride, group_stride;
+};
+
+jattn_status diff_ranges(const jattn_diff_shape* s, DiffRanges* r) {
+  if (s == nullptr) return JATTN_ERR_INVALID_ARG;
+  if (s->B < 0 || s->H < 1 || s->H_kv < 1 || s->S_q < 0 || s->S_kv < 0) return JATTN_ERR_INVALID_ARG;
+  if (s->S_q > (1 << 24) || s->S_kv > (1 << 24) || s->H % s->H_kv != 0) return JATTN_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(s->B) * s->H > 65535) return JATTN_ERR_INVALID_ARG;
+  if (s->d != 64 && s->d != 128) return JATTN_ERR_UNSUPPORTED;
+  const int64_t size[3][3] = {{s->B, s->H, s->S_q}, {s->B, s->H_kv, s->S_kv}, {s->B, s->H_kv, s->S_kv}};
+  const int64_t* stride[3] = {s->q_stride, s->k_stride, s->v_stride};
+  for (int t = 0; t < 3; ++t)
+    for (int i = 0; i < 3; ++i)
+      if (size[t][i] > 1 && (stride[t][i] < s->d || stride[t][i] % 8 != 0 || stride[t][i] >= (int64_t{1} << 38)))
+        return JATTN_ERR_INVALID_ARG;
+  const int G = s->H / s->H_kv;
+  const bool packed = G == 1 || s->S_q == 1 || s->q_stride[1] == s->S_q * s->q_stride[2];
+  r->n_groups = packed ? s->H_kv : s->H;
+  r->hpg = packed ? G : 1;
+  const int64_t rows = static_cast<int64_t>(r->hpg) * s->S_q;
+  r->n_rt = static_cast<int>((rows + 127) / 128);
+  if (rows > INT32_MAX || static_cast<int64_t>(s->B) * r->n_groups * r->n_rt > INT32_MAX) return JATTN_ERR_INVALID_ARG;
+  r->R = static_cast<int>(rows);
+  r->row_stride = s->S_q == 1 ? s->q_stride[1] : s->q_stride[2];
+  r->group_stride = r->hpg * s->q_stride[1];
+  const int64_t items = static_cast<int64_t>(s->B) * r->n_groups * r->n_rt;
+  r->splits = items > 0 ? jattn::diff_splits(items, s->S_kv) : 1;
+  return JATTN_OK;
+}
+
+size_t diff_workspace(const jattn_diff_shape* s, const DiffRanges& r) {
+  if (r.splits == 1) return 0;
+  const size_t rows = static_cast<size_t>(s->B) * s->H * s->S_q;
+  return static_cast<size_t>(r.splits) * 2 * rows * (s->d + 1) * 4;
+}
+
+}  // namespace
+
+namespace jattn {
+
+int device_sm_count() {
+  static int cached[64] = {};
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (cached[dev] > 0) return cached[dev];
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+  cached[dev] = n;
+  return n;
+}
+
+}  // namespace jattn
+
+extern "C" {
+
+jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors, jattn_dtype dtype, int32_t B,
+                          int32_t S, int32_t d, int32_t parts, int32_t rot, const int32_t* pos,
+                          int64_t pos_stride_b, const int32_t* split, const double* freqs,
+                          jattn_rotary_layout layout, float scale, int32_t inverse, void* stream) {
+  if (tensors == nullptr || n_tensors < 1 || n_tensors > 2 || B < 0 || S < 0 || d < 2 || parts < 1)
+    return JATTN_ERR_INVALID_ARG;
+  if (!is_float(dtype)) return JATTN_ERR_UNSUPPORTED;
+  if (layout != JATTN_ROTARY_INTERLEAVED && layout != JATTN_ROTARY_HALF) return JATTN_ERR_INVALID_ARG;
+  if (d % parts != 0 || d / parts % 2 != 0 || rot < 2 || rot % 2 != 0 || rot > d / parts) return JATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale)) return JATTN_ERR_INVALID_ARG;
+  jattn::RotaryParams p{};
+  p.axis_end[0] = p.axis_end[1] = p.axis_end[2] = rot / 2;
+  p.n_axes = 1;
+  if (split != nullptr) {
+    if (split[0] < 0 || split[1] < 0 || split[2] < 0 || ((split[0] | split[1] | split[2]) & 1) != 0 ||
+        static_cast<int64_t>(split[0]) + split[1] + split[2] != rot)
+      return JATTN_ERR_INVALID_ARG;
+    p.n_axes = 3;
+    p.axis_end[0] = split[0] / 2;
+    p.axis_end[1] = (split[0] + split[1]) / 2;
+  }
+  int64_t heads = 0;
+  for (int t = 0; t < n_tensors; ++t) {
+    const jattn_rotary_tensor& x = tensors[t];
+    if (x.H < 0) return JATTN_ERR_INVALID_ARG;
+    heads += x.H;
+    p.H[t] = x.H;
+    p.x[t] = x.x;
+    p.y[t] = x.y;
+    for (int i = 0; i < 3; ++i) {
+      p.xs[t][i] = x.x_stride[i];
+      p.ys[t][i] = x.y_stride[i];
+    }
+  }
+  if (heads * parts > INT32_MAX) return JATTN_ERR_INVALID_ARG;
+  if (B == 0 || S == 0 || heads == 0) return JATTN_OK;
+  if (pos == nullptr || freqs == nullptr) return JATTN_ERR_INVALID_ARG;
+  if (!aligned(pos, 4) || !aligned(freqs, 8)) return JATTN_ERR_ALIGNMENT;
+  for (int t = 0; t < n_tensors; ++t) {
+    if (p.H[t] == 0) continue;
+    if (p.x[t] == nullptr || p.y[t] == nullptr) return JATTN_ERR_INVALID_ARG;
+    if (!aligned(p.x[t], elem_bytes(dtype)) || !aligned(p.y[t], elem_bytes(dtype))) return JATTN_ERR_ALIGNMENT;
+  }
+  p.B = B;
+  p.S = S;
+  p.d = d;
+  p.parts = parts;
+  p.rot = rot;
+  p.pos = pos;
+  p.pos_stride_b = pos_stride_b;
+  p.freqs = freqs;
+  p.scale = scale;
+  p.inverse = inverse != 0;
+  p.tokens = static_cast<long long>(B) * S;
+  return from_cuda(jattn::launch_rotary(p, dtype, layout == JATTN_ROTARY_HALF, static_cast<cudaStream_t>(stream)));
+}
+
+jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void* w, const void* bias,
+                          const void* residual, void* y, void* stream) {
+  if (s == nullptr || s->M < 0 || s->N < 0 || s->K < 1) return JATTN_ERR_INVALID_ARG;
+  if (!is_16bit(s->in_dtype) || !is_float(s->out_dtype)) return JATTN_ERR_UNSUPPORTED;
+  if (bias != nullptr && !is_float(s->bias_dtype)) return JATTN_ERR_UNSUPPORTED;
+  if (s->act < JATTN_ACT_NONE || s->act > JATTN_ACT_RELU) return JATTN_ERR_UNSUPPORTED;
+  if (s->M == 0 || s->N == 0) return JATTN_OK;
+  if (x == nullptr || w == nullptr || y == nullptr) return JATTN_ERR_INVALID_ARG;
+  const int64_t most = int64_t{1} << 38;
+  if (s->ldx < s->K || s->ldw < s->K || s->ldy < s->N || s->ldx >= most || s->ldw >= most || s->ldy >= most)
+    return JATTN_ERR_INVALID_ARG;
+  if (residual != nullptr && (s->ldr < s->N || s->ldr >= most || (residual == y && s->ldr != s->ldy)))
+    return JATTN_ERR_INVALID_ARG;
+  const int ob = elem_bytes(s->out_dtype);
+  if (!aligned(x, 2) || !aligned(w, 2) || !aligned(y, ob)) return JATTN_ERR_ALIGNMENT;
+  if (residual != nullptr && !aligned(residual, ob)) return JATTN_ERR_ALIGNMENT;
+  if (bias != nullptr && !aligned(bias, elem_bytes(s->bias_dtype))) return JATTN_ERR_ALIGNMENT;
+  jattn::LinearParams p{};
+  p.M = s->M;
+  p.N = s->N;
+  p.K = s->K;
+  p.x = static_cast<const uint16_t*>(x);
+  p.w = static_cast<const uint16_t*>(w);
+  p.ldx = s->ldx;
+  p.ldw = s->ldw;
+  p.ldy = s->ldy;
+  p.ldr = s->ldr;
+  p.bias = bias;
+  p.residual = residual;
+  p.y = y;
+  p.in_bf16 = s->in_dtype == JATTN_BF16;
+  p.out_dtype = s->out_dtype;
+  p.bias_dtype = s->bias_dtype;
+  p.act = s->act;
+  p.timeout_ns = kTimeoutNs;
+  p.status = jattn::device_status_ptr();
+  if (p.status == nullptr) return JATTN_ERR_CUDA;
+  // one row needs no stride
+  const bool tma = aligned(x, 16) && aligned(w, 16) && (s->M == 1 || s->ldx % 8 == 0) && (s->N == 1 || s->ldw % 8 == 0);
+  const jattn::LinearPlan plan = jattn::plan_linear(s->M, s->N, s->K, tma);
+  CUtensorMap tx{}, tw{};
+  if (tma) {
+    const int bx = plan.pair ? 128 : (plan.swap ? plan.bn : 128), bw = plan.pair ? 128 : (plan.swap ? 128 : plan.bn);
+    if (!matrix_map(&tx, x, s->M, s->K, s->ldx, bx) || !matrix_map(&tw, w, s->N, s->K, s->ldw, bw)) return JATTN_ERR_CUDA;
+  }
+  return from_cuda(jattn::launch_linear(p, plan, tma, tx, tw, static_cast<cudaStream_t>(stream)));
+}
+
+size_t jattn_fwd_diff_workspace(const jattn_diff_shape* shape) {
+  DiffRanges r;
+  return diff_ranges(shape, &r) == JATTN_OK ? diff_workspace(shape, r) : 0;
+}
+
+jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, const void* q, const void* k, const void* v,
+                            const float* lam, float lambda_init, const float* norm_w, float eps,
+                            const int32_t* kv_len, const uint8_t* key_mask, void* workspace, size_t workspace_bytes,
+                            void* o, float* lse, float softmax_scale, void* stream) {
+  if (!is_16bit(in_dtype)) return JATTN_ERR_UNSUPPORTED;
+  DiffRanges r;
+  const jattn_status st = diff_ranges(s, &r);
+  if (st != JATTN_OK) return st;
+  if (!std::isfinite(softmax_scale) || !std::isfinite(lambda_init)) return JATTN_ERR_INVALID_ARG;
+  if (norm_w != nullptr && (!(eps > 0.f) || !std::isfinite(eps))) return JATTN_ERR_INVALID_ARG;
+  if (s->B == 0 || s->S_q == 0) return JATTN_OK;
+  if (q == nullptr || lam == nullptr || o == nullptr) return JATTN_ERR_INVALID_ARG;
+  if (s->S_kv > 0 && (k == nullptr || v == nullptr)) return JATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lam, 16) ||
+      !aligned(norm_w, 16) || !aligned(kv_len, 4) || !aligned(lse, 4))
+    return JATTN_ERR_ALIGNMENT;
+  const size_t need = diff_workspace(s, r);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return JATTN_ERR_INVALID_ARG;
+  if (need > 0 && !aligned(workspace, 256)) return JATTN_ERR_ALIGNMENT;
+  const int64_t items = static_cast<int64_t>(s->B) * r.n_groups * r.n_rt * r.splits;
+  if (items > INT32_MAX) return JATTN_ERR_INVALID_ARG;
+  jattn::DiffParams p{};
+  p.B = s->B;
+  p.H = s->H;
+  p.H_kv = s->H_kv;
+  p.S_q = s->S_q;
+  p.S_kv = s->S_kv;
+  p.n_groups = r.n_groups;
+  p.hpg = r.hpg;
+  p.R = r.R;
+  p.n_rt = r.n_rt;
+  p.splits = r.splits;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(0.5f * static_cast<float>(s->d));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.lam = lam;
+  p.lambda_init = lambda_init;
+  p.norm_w = norm_w;
+  p.eps = eps;
+  p.kv_len = kv_len;
+  p.key_mask = key_mask;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  if (r.splits > 1) {
+    const size_t rows = static_cast<size_t>(s->B) * s->H * s->S_q;
+    p.part_o = static_cast<float*>(workspace);
+    p.part_l = p.part_o + static_cast<size_t>(r.splits) * 2 * rows * s->d;
+  }
+  p.timeout_ns = kTimeoutNs;
+  p.status = jattn::device_status_ptr();
+  if (p.status == nullptr) return JATTN_ERR_CUDA;
+  CUtensorMap tq, tk, tv;
+  // without keys nothing is loaded: any valid address does
+  const void* kb = s->S_kv > 0 ? k : q;
+  const void* vb = s->S_kv > 0 ? v : q;
+  const int64_t skv = s->S_kv > 0 ? s->S_kv : 1;
+  if (!heads_map(&tq, q, s->d, r.R, r.n_groups, s->B, r.row_stride, r.group_stride, s->q_stride[0]) ||
+      !heads_map(&tk, kb, s->d, skv, s->H_kv, s->B, s->k_stride[2], s->k_stride[1], s->k_stride[0]) ||
+      !heads_map(&tv, vb, s->d, skv, s->H_kv, s->B, s->v_stride[2], s->v_stride[1], s->v_stride[0]))
+    return JATTN_ERR_CUDA;
+  return from_cuda(jattn::launch_diff_attn(p, s->d, in_dtype == JATTN_BF16, tq, tk, tv,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

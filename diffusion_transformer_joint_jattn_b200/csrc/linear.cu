@@ -1,0 +1,744 @@
+// Linear layer on sm_100a: y = act(x W^T + bias) + residual, 16-bit operands,
+// fp32 accumulation in tensor memory, the epilogue fused.
+//
+// Two kernels share the epilogue:
+//   pair   256 x 256 output tiles by a cluster of two CTAs (cta_group::2):
+//          each CTA holds 128 rows of x and 128 rows of W per 64-deep K step,
+//          so an operand byte in shared memory feeds twice the MACs of a
+//          single-CTA tile; persistent, two accumulators in TMEM, so one
+//          tile's epilogue overlaps the next tile's products.
+//   tile   128 x BN output tiles by one CTA, for problems with too few 256 x
+//          256 tiles to fill the GPU; K may be split over a cluster of up to
+//          8 CTAs that add their accumulators through distributed shared
+//          memory (in rank order: same bits every run, no workspace).  Few
+//          rows of x: the roles are swapped (W's rows are the MMA's 128 rows,
+//          x the BN), so the tile wastes no work on absent rows and W streams
+//          once.  Operands that TMA cannot address (row strides that are not
+//          multiples of 16 bytes) are staged by plain loads instead.
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "jattn.h"
+#include "jattn_internal.h"
+#include "ptx_sm100.cuh"
+
+namespace jattn {
+
+namespace {
+
+constexpr int BK = 64;                 // K per stage: one 128-byte swizzle row
+constexpr int kEpiThreads = 128;       // warps 0..3
+constexpr int kThreads = 192;          // + warp 4 (loads), warp 5 (MMA)
+
+struct __align__(8) TileBars {
+  uint64_t full[8], empty[8];
+  uint64_t acc_full[2], acc_empty[2];
+  uint32_t tmem_base;
+  uint32_t abort;
+};
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, bool bf16) {
+  if (bf16) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ float widen16(uint16_t u, bool bf16) {
+  return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16) : __half2float(__ushort_as_half(u));
+}
+// One element of type dt at index i.
+__device__ __forceinline__ float load_as_f32(const void* p, int64_t i, int dt) {
+  if (dt == JATTN_FP32) return static_cast<const float*>(p)[i];
+  return widen16(static_cast<const uint16_t*>(p)[i], dt == JATTN_BF16);
+}
+__device__ __forceinline__ void store_from_f32(void* p, int64_t i, int dt, float v) {
+  if (dt == JATTN_FP32) static_cast<float*>(p)[i] = v;
+  else if (dt == JATTN_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// The activations, in fp32.  exp and the reciprocal are the hardware's
+// approximate ones (2^-21 relative or better, far under the 16-bit output's
+// rounding and at the level of the fp32 sum's own).
+__device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float activate(float x, int act) {
+  switch (act) {
+    case JATTN_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+    // 0.5 (1 + tanh u) = sigmoid(2 u)
+    case JATTN_ACT_GELU_TANH: return x * sigmoid_f32(1.5957691216057308f * (x + 0.044715f * x * x * x));
+    case JATTN_ACT_SILU: return x * sigmoid_f32(x);
+    case JATTN_ACT_RELU: return x < 0.f ? 0.f : x;     // keeps NaN
+    default: return x;
+  }
+}
+
+// Whether 32-element chunks of a row-major matrix (type dt, row stride ld)
+// may be moved with 16- or 32-byte accesses: bytes of the widest, else 0.
+__host__ __device__ inline int vector_bytes(const void* p, int64_t ld, int dt) {
+  const int64_t es = dt == JATTN_FP32 ? 4 : 2;
+  const uint64_t m = reinterpret_cast<uint64_t>(p) | static_cast<uint64_t>(ld * es);
+  return (m & 31) == 0 ? 32 : ((m & 15) == 0 ? 16 : 0);
+}
+
+template <int WORDS>
+__device__ __forceinline__ void load_row(const uint32_t* src, uint32_t (&w)[WORDS], int vec) {
+  if (vec == 32) {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 8)
+      asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
+                     "=r"(w[i + 6]), "=r"(w[i + 7])
+                   : "l"(src + i)
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4) {
+      const uint4 t = *reinterpret_cast<const uint4*>(src + i);
+      w[i] = t.x; w[i + 1] = t.y; w[i + 2] = t.z; w[i + 3] = t.w;
+    }
+  }
+}
+template <int WORDS>
+__device__ __forceinline__ void store_row(uint32_t* dst, const uint32_t (&w)[WORDS], int vec) {
+  if (vec == 32) {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                   ::"l"(dst + i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                     "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4) *reinterpret_cast<uint4*>(dst + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+}
+
+// Columns [n, n + 32) of row m from the accumulator, bias already fp32 in
+// shared memory (zeros past N or without a bias).
+__device__ __forceinline__ void finish_row(const LinearParams& p, float (&v)[32], const float* bias, int64_t m, int n) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = activate(v[i] + bias[i], p.act);
+  const bool f32 = p.out_dtype == JATTN_FP32, bf16 = p.out_dtype == JATTN_BF16;
+  const bool whole = n + 32 <= p.N;
+  if (p.residual != nullptr) {
+    const int64_t at = m * p.ldr + n;
+    if (whole && p.vec_r != 0) {
+      if (f32) {
+        uint32_t w[32];
+        load_row(static_cast<const uint32_t*>(p.residual) + at, w, p.vec_r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(w[i]);
+      } else {
+        uint32_t w[16];
+        load_row(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.residual) + at), w, p.vec_r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          v[2 * i] += widen16(static_cast<uint16_t>(w[i]), bf16);
+          v[2 * i + 1] += widen16(static_cast<uint16_t>(w[i] >> 16), bf16);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (n + i < p.N) v[i] += load_as_f32(p.residual, at + i, p.out_dtype);
+    }
+  }
+  const int64_t at = m * p.ldy + n;
+  if (whole && p.vec_y != 0) {
+    if (f32) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+      store_row(static_cast<uint32_t*>(p.y) + at, w, p.vec_y);
+    } else {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], bf16);
+      store_row(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + at), w, p.vec_y);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (n + i < p.N) store_from_f32(p.y, at + i, p.out_dtype, v[i]);
+  }
+}
+
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Address of the same shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Bounded wait of a whole warp (the tcgen05.ld that follows is collective).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    const bool ok = mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if ((i & 63u) == 0u) {
+      int stop = 0;
+      if (lane_id() == 0) {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (*ctl.abort) {
+          stop = 1;
+        } else if (now - t0 > ctl.limit_ns) {
+          atomicOr(ctl.status, JATTN_DEV_TIMEOUT);
+          *ctl.abort = 1u;
+          stop = 1;
+        }
+      }
+      if (__shfl_sync(0xffffffffu, stop, 0)) return false;
+    }
+  }
+}
+// After an abort: leave copies in flight time to land before the CTA's
+// shared memory goes away (they need microseconds).
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < 1000000ull) {
+  }
+}
+
+// 16 columns per lane, into the first half of r.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint64_t* bar, void* dst, int32_t c0, int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+      : "memory");
+}
+// Into this CTA's shared memory, counted on the pair's leader's barrier (the
+// peer bit of the barrier address cleared).
+__device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint64_t* bar, void* dst, int32_t c0,
+                                                 int32_t c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar) & 0xFEFFFFFFu), "r"(c0), "r"(c1)
+      : "memory");
+}
+
+// ---------------------------------------------------------------- one-CTA tiles
+
+// SWAP: the MMA's 128 rows are W's and its BN columns x's; TMA: operands by
+// TMA, else by plain loads of the epilogue warps.
+template <int BN, bool SWAP, bool TMA>
+struct TileCfg {
+  static constexpr int STAGE = (128 + BN) * BK * 2;
+  static constexpr int ST = BN >= 128 ? 3 : (BN >= 64 ? 4 : 5);
+  static constexpr int PIPE = ST * STAGE;
+  static constexpr int RED = 128 * BN * 4;              // split K: this CTA's accumulator tile
+  static constexpr int DATA = PIPE > RED ? PIPE : RED;
+  static constexpr int SMEM = DATA + BN * 4 + 512 + 1024;
+  static constexpr uint32_t TCOLS = BN < 32 ? 32u : static_cast<uint32_t>(BN);
+};
+
+// Stage rows [row0, row0 + rows) x [k0, k0 + 64) of a [n_rows][K] matrix in
+// the 128-byte swizzled layout, zeros outside; lane = two neighbouring k.
+__device__ __forceinline__ void stage_plain(const uint16_t* g, int64_t ld, int64_t row0, int rows, int64_t n_rows, int k0,
+                                            int K, uint8_t* dst) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k = k0 + 2 * lane;
+#pragma unroll 8
+  for (int r = warp; r < rows; r += 4) {
+    uint32_t lo = 0, hi = 0;
+    if (row0 + r < n_rows) {
+      const uint16_t* src = g + (row0 + r) * ld + k;
+      if (k < K) lo = __ldg(src);
+      if (k + 1 < K) hi = __ldg(src + 1);
+    }
+    const uint32_t off = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2);
+    *reinterpret_cast<uint32_t*>(dst + off) = lo | (hi << 16);
+  }
+}
+
+template <int BN, bool SWAP, bool TMA>
+__global__ void __launch_bounds__(kThreads)
+linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const LinearParams p) {
+  using C = TileCfg<BN, SWAP, TMA>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* sBias = reinterpret_cast<float*>(smem + C::DATA);
+  TileBars* bar = reinterpret_cast<TileBars*>(smem + C::DATA + BN * 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // tile (a, b) = rows a * 128 of A, rows b * BN of B; the cluster's CTAs
+  // share a tile and take the K steps [kb, ke)
+  const int split = p.splits, rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int tile = blockIdx.x / split;
+  const int ta = tile % p.tiles_a, tb = tile / p.tiles_a;
+  const int ksteps = (p.K + BK - 1) / BK;
+  const int kb = static_cast<int>(static_cast<long long>(ksteps) * rank / split);
+  const int ke = static_cast<int>(static_cast<long long>(ksteps) * (rank + 1) / split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(&bar->full[s], TMA ? 1 : kEpiThreads);
+      mbar_init(&bar->empty[s], 1);
+    }
+    mbar_init(&bar->acc_full[0], 1);
+    bar->abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 5) {
+    __syncwarp();
+    tmem_alloc(&bar->tmem_base, C::TCOLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  const WaitCtl ctl{&bar->abort, p.status, p.timeout_ns};
+
+  if (warp == 4) {
+    if (TMA && lane == 0) {
+      bool ok = true;
+      for (int k = kb; k < ke && ok; ++k) {
+        const int i = k - kb, s = i % C::ST;
+        ok = mbar_wait(&bar->empty[s], ((i / C::ST) & 1) ^ 1, ctl);
+        if (!ok) break;
+        mbar_arrive_expect_tx(&bar->full[s], C::STAGE);
+        tma_load_2d(&tmA, &bar->full[s], smem + s * C::STAGE, k * BK, ta * 128);
+        tma_load_2d(&tmB, &bar->full[s], smem + s * C::STAGE + 128 * BK * 2, k * BK, tb * BN);
+      }
+      // the last stages' commits have arrived before the CTA may exit
+      for (int i = ke - kb > C::ST ? ke - kb - C::ST : 0; i < ke - kb && ok; ++i)
+        ok = mbar_wait(&bar->empty[i % C::ST], (i / C::ST) & 1, ctl);
+      if (!ok) settle();
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = instr_desc(p.in_bf16, p.in_bf16, 0, 128, BN);
+      for (int k = kb; k < ke; ++k) {
+        const int i = k - kb, s = i % C::ST;
+        if (!mbar_wait(&bar->full[s], (i / C::ST) & 1, ctl)) break;
+        tc_fence_after();
+        const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + 128 * BK * 2;
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          mma_f16_ss(tmem, smem_desc(a + kk * 32, 16, 1024, 2u), smem_desc(b + kk * 32, 16, 1024, 2u), idesc,
+                     i > 0 || kk > 0);
+        mma_commit(&bar->empty[s]);
+      }
+      mma_commit(&bar->acc_full[0]);
+    }
+  } else {
+    if (!TMA) {
+      bool ok = true;
+      for (int k = kb; k < ke && ok; ++k) {
+        const int i = k - kb, s = i % C::ST;
+        ok = warp_wait(&bar->empty[s], ((i / C::ST) & 1) ^ 1, ctl);
+        if (!ok) break;
+        uint8_t* dst = smem + s * C::STAGE;
+        stage_plain(p.a, p.lda, static_cast<int64_t>(ta) * 128, 128, p.rows_a, k * BK, p.K, dst);
+        stage_plain(p.b, p.ldb, static_cast<int64_t>(tb) * BN, BN, p.rows_b, k * BK, p.K, dst + 128 * BK * 2);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        mbar_arrive(&bar->full[s]);
+      }
+    }
+    if (!SWAP) {
+      for (int i = threadIdx.x; i < BN; i += kEpiThreads) {
+        const int n = tb * BN + i;
+        sBias[i] = p.bias != nullptr && n < p.N ? load_as_f32(p.bias, n, p.bias_dtype) : 0.f;
+      }
+      epi_sync();
+    }
+  }
+  // The epilogue waits for the accumulator; every thread then meets the
+  // cluster's other CTAs (or the block) once.
+  bool good = false;
+  const int row = (warp & 3) * 32 + lane;
+  const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+  if (warp < 4) {
+    good = warp_wait(&bar->acc_full[0], 0, ctl);
+    __syncwarp();
+    tc_fence_after();
+  }
+  constexpr int CH = BN < 32 ? BN : 32;                  // accumulator columns at a time
+  float* red = reinterpret_cast<float*>(smem);           // [BN][128]: the pipeline is drained
+  __syncwarp();
+  if (split > 1) {
+    if (warp < 4 && good) {
+#pragma unroll
+      for (int c = 0; c < BN; c += CH) {
+        uint32_t r[32];
+        if constexpr (CH == 16) tmem_ld16(tl + c, r);
+        else tmem_ld32(tl + c, r);
+#pragma unroll
+        for (int i = 0; i < CH; ++i) red[(c + i) * 128 + row] = __uint_as_float(r[i]);
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  if (warp < 4 && good) {
+    // the columns of this CTA: all, or its share of a split tile
+    const int c_lo = split > 1 ? BN * rank / split : 0;
+    const int c_hi = split > 1 ? BN * (rank + 1) / split : BN;
+    const uint32_t red_addr = smem_u32(red);
+    if (SWAP) {
+      const int64_t n = static_cast<int64_t>(ta) * 128 + row;
+      const float bias = p.bias != nullptr && n < p.N ? load_as_f32(p.bias, n, p.bias_dtype) : 0.f;
+      auto put = [&](int c, float v) {
+        const int64_t m = static_cast<int64_t>(tb) * BN + c;
+        if (m < p.M && n < p.N) {
+          v = activate(v + bias, p.act);
+          if (p.residual != nullptr) v += load_as_f32(p.residual, m * p.ldr + n, p.out_dtype);
+          store_from_f32(p.y, m * p.ldy + n, p.out_dtype, v);
+        }
+      };
+      if (split > 1) {
+        for (int c = c_lo; c < c_hi; ++c) {
+          float v = 0.f;
+          for (int q = 0; q < split; ++q) v += ld_cluster(map_rank(red_addr + (c * 128 + row) * 4, q));
+          put(c, v);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < BN; c += CH) {
+          uint32_t r[32];
+          __syncwarp();
+          if constexpr (CH == 16) tmem_ld16(tl + c, r);
+          else tmem_ld32(tl + c, r);
+#pragma unroll
+          for (int i = 0; i < CH; ++i) put(c + i, __uint_as_float(r[i]));
+        }
+      }
+    } else if constexpr (BN >= 32) {
+      const int64_t m = static_cast<int64_t>(ta) * 128 + row;
+      if (split > 1) {
+        // a share narrower than 32 columns is finished one element at a time
+        for (int c = c_lo; c < c_hi; c += 32) {
+          const int w = min(32, c_hi - c);
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int q = 0; q < split; ++q) {
+            const uint32_t at = map_rank(red_addr + (c * 128 + row) * 4, q);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < w) v[i] += ld_cluster(at + i * 512);
+          }
+          if (m < p.M) {
+            if (w == 32) {
+              finish_row(p, v, sBias + c, m, tb * BN + c);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int n = tb * BN + c + i;
+                if (i < w && n < p.N) {
+                  float t = activate(v[i] + sBias[c + i], p.act);
+                  if (p.residual != nullptr) t += load_as_f32(p.residual, m * p.ldr + n, p.out_dtype);
+                  store_from_f32(p.y, m * p.ldy + n, p.out_dtype, t);
+                }
+              }
+            }
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(tl + c, r);
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          if (m < p.M && tb * BN + c < p.N) finish_row(p, v, sBias + c, m, tb * BN + c);
+        }
+      }
+    }
+  }
+  // no CTA leaves while another still reads its accumulators
+  __syncwarp();
+  if (split > 1) cluster_sync();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TCOLS);
+  }
+}
+
+// ---------------------------------------------------------------- pairs of CTAs
+
+struct PairCfg {
+  static constexpr int STAGE = (128 + 128) * BK * 2;     // per CTA: its rows of x, its rows of W
+  static constexpr int ST = 6;
+  static constexpr int BIAS = 4 * 256 * 4;               // each epilogue warp keeps its own copy
+  static constexpr int SMEM = ST * STAGE + BIAS + 512 + 1024;
+};
+constexpr int kGroupM = 8;                               // tiles of x a column of W tiles is used for in a row
+
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                   const LinearParams p) {
+  using C = PairCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* sBias = reinterpret_cast<float*>(smem + C::ST * C::STAGE);   // [4][256]
+  TileBars* bar = reinterpret_cast<TileBars*>(smem + C::ST * C::STAGE + C::BIAS);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int tiles_n = (p.N + 255) / 256;
+  const long long n_tiles = static_cast<long long>(p.tiles_a) * tiles_n;
+  const int n_pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int ksteps = (p.K + BK - 1) / BK;
+  // tile order: kGroupM row tiles share each column tile while both are in L2
+  auto place = [&](long long t, int& tm, int& tn) {
+    const long long per = static_cast<long long>(kGroupM) * tiles_n;
+    const int g = static_cast<int>(t / per), first = g * kGroupM;
+    const int size = min(kGroupM, p.tiles_a - first), in = static_cast<int>(t % per);
+    tm = first + in % size;
+    tn = in / size;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::ST; ++s) {
+      mbar_init(&bar->full[s], 1);
+      mbar_init(&bar->empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->acc_full[i], 1);
+      mbar_init(&bar->acc_empty[i], 8);                  // four epilogue warps of both CTAs
+    }
+    bar->abort = 0;
+    fence_mbarrier_init();
+  }
+  cluster_sync();
+  if (warp == 5) {
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                 ::"r"(smem_u32(&bar->tmem_base)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem_base;
+  const WaitCtl ctl{&bar->abort, p.status, p.timeout_ns};
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (long long t = pair; t < n_tiles && ok; t += n_pairs) {
+        int tm, tn;
+        place(t, tm, tn);
+        for (int k = 0; k < ksteps; ++k, ++it) {
+          const int s = it % C::ST;
+          ok = mbar_wait(&bar->empty[s], ((it / C::ST) & 1) ^ 1, ctl);
+          if (!ok) break;
+          if (leader) mbar_arrive_expect_tx(&bar->full[s], 2 * C::STAGE);
+          uint8_t* dst = smem + s * C::STAGE;
+          tma_load_2d_pair(&tmX, &bar->full[s], dst, k * BK, tm * 256 + static_cast<int>(rank) * 128);
+          tma_load_2d_pair(&tmW, &bar->full[s], dst + 128 * BK * 2, k * BK, tn * 256 + static_cast<int>(rank) * 128);
+        }
+      }
+      // the last stages' commits have arrived before the CTA may exit
+      for (int i = it > C::ST ? it - C::ST : 0; i < it && ok; ++i)
+        ok = mbar_wait(&bar->empty[i % C::ST], (i / C::ST) & 1, ctl);
+      if (!ok) settle();
+    }
+  } else if (warp == 5) {
+    if (leader && lane == 0) {
+      const uint32_t idesc = instr_desc(p.in_bf16, p.in_bf16, 0, 256, 256);
+      int it = 0, n = 0;
+      bool ok = true;
+      for (long long t = pair; t < n_tiles && ok; t += n_pairs, ++n) {
+        const int buf = n & 1;
+        ok = mbar_wait(&bar->acc_empty[buf], ((n >> 1) & 1) ^ 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        for (int k = 0; k < ksteps; ++k, ++it) {
+          const int s = it % C::ST;
+          ok = mbar_wait(&bar->full[s], (it / C::ST) & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + 128 * BK * 2;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = smem_desc(a + kk * 32, 16, 1024, 2u), bd = smem_desc(b + kk * 32, 16, 1024, 2u);
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.ne.b32 p, %4, 0;\n\t"
+                "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+                ::"r"(tmem + buf * 256u), "l"(ad), "l"(bd), "r"(idesc), "r"(static_cast<uint32_t>(k > 0 || kk > 0))
+                : "memory");
+          }
+          asm volatile(
+              "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+              ::"r"(smem_u32(&bar->empty[s])), "h"(static_cast<uint16_t>(3)) : "memory");
+        }
+        if (!ok) break;
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(smem_u32(&bar->acc_full[buf])), "h"(static_cast<uint16_t>(3)) : "memory");
+      }
+      if (!ok) settle();
+    }
+  } else {
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    int n = 0;
+    for (long long t = pair; t < n_tiles; t += n_pairs, ++n) {
+      int tm, tn;
+      place(t, tm, tn);
+      const int buf = n & 1;
+      // no barrier among the epilogue warps: one that gave up must not leave
+      // the others waiting for it
+      float* bias = sBias + warp * 256;
+      __syncwarp();
+      for (int i = lane; i < 256; i += 32) {
+        const int c = tn * 256 + i;
+        bias[i] = p.bias != nullptr && c < p.N ? load_as_f32(p.bias, c, p.bias_dtype) : 0.f;
+      }
+      if (!warp_wait(&bar->acc_full[buf], (n >> 1) & 1, ctl)) break;
+      __syncwarp();
+      tc_fence_after();
+      const int64_t m = static_cast<int64_t>(tm) * 256 + rank * 128 + warp * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld32(tl + buf * 256 + c, r);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if (m < p.M && tn * 256 + c < p.N) finish_row(p, v, bias + c, m, tn * 256 + c);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                     ::"r"(map_rank(smem_u32(&bar->acc_empty[buf]), 0)) : "memory");
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (warp == 5) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+template <int BN, bool SWAP, bool TMA>
+cudaError_t launch_tile(const LinearParams& p, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st) {
+  using C = TileCfg<BN, SWAP, TMA>;
+  auto kern = linear_tile_kernel<BN, SWAP, TMA>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long blocks = static_cast<long long>(p.tiles_a) * p.tiles_b * p.splits;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
+}
+
+}  // namespace
+
+// The kernel, tile and split of one problem: pure host arithmetic.
+LinearPlan plan_linear(int M, int N, int K, bool tma) {
+  LinearPlan pl{};
+  const long long ksteps = (K + BK - 1) / BK;
+  const long long pair_tiles = static_cast<long long>((M + 255) / 256) * ((N + 255) / 256);
+  if (tma && pair_tiles >= 74) {
+    pl.pair = true;
+    return pl;
+  }
+  long long tiles;
+  if (M <= 64) {
+    pl.swap = true;
+    pl.bn = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
+    tiles = static_cast<long long>((N + 127) / 128) * ((M + pl.bn - 1) / pl.bn);
+  } else {
+    pl.bn = 128;
+    tiles = static_cast<long long>((M + 127) / 128) * ((N + 127) / 128);
+    if (tiles < 148 || N <= 64) {
+      pl.bn = 64;
+      tiles = static_cast<long long>((M + 127) / 128) * ((N + 63) / 64);
+    }
+  }
+  pl.splits = 1;
+  while (pl.splits < 8 && tiles * pl.splits * 2 <= 296 && ksteps / (pl.splits * 2) >= 4) pl.splits *= 2;
+  return pl;
+}
+
+cudaError_t launch_linear(LinearParams p, const LinearPlan& pl, bool tma, const CUtensorMap& tx, const CUtensorMap& tw,
+                          cudaStream_t st) {
+  p.vec_y = vector_bytes(p.y, p.ldy, p.out_dtype);
+  p.vec_r = p.residual != nullptr ? vector_bytes(p.residual, p.ldr, p.out_dtype) : 0;
+  if (pl.pair) {
+    p.tiles_a = (p.M + 255) / 256;
+    cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::SMEM);
+    if (e != cudaSuccess) return e;
+    const long long n_tiles = static_cast<long long>(p.tiles_a) * ((p.N + 255) / 256);
+    const long long pairs = device_sm_count() / 2;
+    const int grid = static_cast<int>(2 * (n_tiles < pairs ? n_tiles : pairs));
+    linear_pair_kernel<<<grid, kThreads, PairCfg::SMEM, st>>>(tx, tw, p);
+    return cudaGetLastError();
+  }
+  p.splits = pl.splits;
+  const int rows_a = pl.swap ? p.N : p.M, rows_b = pl.swap ? p.M : p.N;
+  p.tiles_a = (rows_a + 127) / 128;
+  p.tiles_b = (rows_b + pl.bn - 1) / pl.bn;
+  p.rows_a = rows_a;
+  p.rows_b = rows_b;
+  p.a = pl.swap ? p.w : p.x;
+  p.b = pl.swap ? p.x : p.w;
+  p.lda = pl.swap ? p.ldw : p.ldx;
+  p.ldb = pl.swap ? p.ldx : p.ldw;
+  const CUtensorMap& ta = pl.swap ? tw : tx;
+  const CUtensorMap& tb = pl.swap ? tx : tw;
+  if (pl.swap) {
+    if (pl.bn == 16) return tma ? launch_tile<16, true, true>(p, ta, tb, st) : launch_tile<16, true, false>(p, ta, tb, st);
+    if (pl.bn == 32) return tma ? launch_tile<32, true, true>(p, ta, tb, st) : launch_tile<32, true, false>(p, ta, tb, st);
+    return tma ? launch_tile<64, true, true>(p, ta, tb, st) : launch_tile<64, true, false>(p, ta, tb, st);
+  }
+  if (pl.bn == 64) return tma ? launch_tile<64, false, true>(p, ta, tb, st) : launch_tile<64, false, false>(p, ta, tb, st);
+  return tma ? launch_tile<128, false, true>(p, ta, tb, st) : launch_tile<128, false, false>(p, ta, tb, st);
+}
+
+}  // namespace jattn

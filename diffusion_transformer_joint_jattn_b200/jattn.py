@@ -13,6 +13,10 @@ Entry points mirror the C names:
   rope_qkv_hp / fwd_bf16_hp   the high-precision 16-bit path (range scales,
                split-precision Q.K^T on the outlier channel pairs)
   joint_attention  the whole path in one call (host or device tensors)
+and of the layer around the attention:
+  rotary       rotary embedding of strided q and k (rotary_freqs: its table)
+  linear       matrix product with bias, activation and residual
+  fwd_diff     differential attention, with lengths, key mask, shared heads
 """
 from __future__ import annotations
 
@@ -28,7 +32,7 @@ LIB_PATH = os.path.join(_PKG, "libjattn.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_ALIGNMENT, ERR_CUDA, ERR_TIMEOUT, ERR_RANGE, ERR_INTERNAL = range(8)
 DEV_TIMEOUT, DEV_RANGE, DEV_CHECK = 1, 2, 4
-BF16, FP16, E4M3 = 0, 1, 2
+BF16, FP16, E4M3, FP32 = 0, 1, 2, 3
 BLOCK = 128
 
 _DTYPE_CODE = {torch.bfloat16: BF16, torch.float16: FP16, torch.float8_e4m3fn: E4M3}
@@ -40,6 +44,7 @@ SYMBOLS = ("jattn_rope_qkv", "jattn_rope_qkv_norm", "jattn_quant_fp8", "jattn_fw
            "jattn_joint_attention_host", "jattn_joint_attention_host_workspace", "jattn_fwd_bf16", "jattn_fwd_fp8",
            "jattn_rope_qkv_hp", "jattn_rope_qkv_hp_workspace", "jattn_fwd_bf16_hp",
            "jattn_fwd_block_sparse", "jattn_fwd_block_sparse_workspace",
+           "jattn_rotary", "jattn_linear", "jattn_fwd_diff", "jattn_fwd_diff_workspace",
            "jattn_device_status", "jattn_last_device_status", "jattn_selftest_wait_timeout", "jattn_status_string",
            "jattn_version")
 
@@ -47,6 +52,24 @@ SYMBOLS = ("jattn_rope_qkv", "jattn_rope_qkv_norm", "jattn_quant_fp8", "jattn_fw
 class Shape(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("S_txt", ctypes.c_int32),
                 ("S_img", ctypes.c_int32), ("S_ref", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class RotaryTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
+
+
+class LinearShape(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("ldx", ctypes.c_int64),
+                ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("bias_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32)]
+
+
+class DiffShape(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("S_q", ctypes.c_int32),
+                ("S_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 3),
+                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3)]
 
 
 class JattnError(RuntimeError):
@@ -89,6 +112,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jattn_fwd_block_sparse.argtypes = [sp, i32, vp, vp, vp, f32, vp, ctypes.c_size_t, vp, vp, vp, vp, f32, vp]
     lib.jattn_fwd_block_sparse_workspace.argtypes = [sp]
     lib.jattn_fwd_fp8.argtypes = [sp, vp, vp, vp, vp, vp, vp, f32, vp]
+    lib.jattn_rotary.argtypes = [ctypes.POINTER(RotaryTensor), i32, i32, i32, i32, i32, i32, i32, vp, ctypes.c_int64,
+                                 ctypes.POINTER(i32), vp, i32, f32, i32, vp]
+    lib.jattn_linear.argtypes = [ctypes.POINTER(LinearShape), vp, vp, vp, vp, vp, vp]
+    lib.jattn_fwd_diff.argtypes = [ctypes.POINTER(DiffShape), i32, vp, vp, vp, vp, f32, vp, f32, vp, vp, vp,
+                                   ctypes.c_size_t, vp, vp, f32, vp]
+    lib.jattn_fwd_diff_workspace.argtypes = [ctypes.POINTER(DiffShape)]
     lib.jattn_device_status.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_uint32)]
     lib.jattn_last_device_status.argtypes = [vp]
     lib.jattn_selftest_wait_timeout.argtypes = [i32, vp]
@@ -102,6 +131,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jattn_rope_qkv_hp_workspace.restype = ctypes.c_size_t
     lib.jattn_fwd_block_sparse_workspace.restype = ctypes.c_size_t
     lib.jattn_joint_attention_host_workspace.restype = ctypes.c_size_t
+    lib.jattn_fwd_diff_workspace.restype = ctypes.c_size_t
     _lib = lib
     return lib
 
@@ -591,6 +621,295 @@ def joint_attention(qkv_txt, qkv_img, qkv_ref, pos, split, theta: float = 10000.
     else:
         raise ValueError(f"unknown path {path!r}")
     return (o, lse) if want_lse else o
+
+
+# ---------------------------------------------------------------- the layer around the attention
+
+_FLOAT_CODE = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+_ACT_CODE = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
+_ROTARY_LAYOUT = {"interleaved": 0, "half": 1}
+_I64x3 = ctypes.c_int64 * 3
+
+
+def _enqueue(dev, stream, inputs, call):
+    """``call(stream pointer)`` with ``dev`` current and the stream given (the
+    device's current one when None).  On a stream that is not the current one
+    the outputs are allocated for that stream, and the inputs are kept from
+    reuse until its work is done."""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(dev):
+        if stream is None or stream == torch.cuda.current_stream():
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(stream):
+            out = call(stream.cuda_stream)
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        return out
+
+
+def _on(t, name: str, dev, dtypes):
+    """``t`` is a tensor on the CUDA device ``dev`` of one of ``dtypes``."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+
+
+def _cuda_device(t, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def rotary_freqs(dim=None, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_length: int = 4096, fast_turns: float = 32.0, slow_turns: float = 1.0, split=None,
+                 device=None):
+    """Frequencies (fp64 tensor [dim / 2], radians per position) and the factor
+    of cosine and sine for ``rotary``: (freqs, scale).
+
+    Pair i of a span of n channels turns theta^(-2i/n) per position.  ``split``:
+    the channels of the t, row and col axes (one span each; dim is their sum).
+    Longer contexts than ``original_length`` by ``factor``:
+      linear  every frequency divided by the factor (positions interpolated)
+      ntk     theta * factor^(n / (n - 2)): the slowest pair is interpolated,
+              the fastest keeps its frequency
+      yarn    pairs that turn at least ``fast_turns`` times over the original
+              length keep their frequency, those below ``slow_turns`` are
+              interpolated, a linear ramp between; scale 0.1 ln(factor) + 1.
+    """
+    if scaling not in ("none", "linear", "ntk", "yarn"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not theta > 0 or not math.isfinite(theta) or not factor > 0 or not math.isfinite(factor):
+        raise ValueError("theta and factor must be positive")
+    spans = [dim] if split is None else [int(n) for n in split]
+    if split is not None and (len(spans) != 3 or scaling != "none" or (dim is not None and dim != sum(spans))):
+        raise ValueError("split is three channel counts that sum to dim, without scaling")
+    if any(n is None or n < 0 or n % 2 for n in spans) or sum(spans) < 2:
+        raise ValueError("channel counts must be even and at least 2 in all")
+    scale, freqs = 1.0, []
+    for n in spans:
+        i = torch.arange(n // 2, dtype=torch.float64)
+        base = theta * factor ** (n / max(1, n - 2)) if scaling == "ntk" else theta
+        w = base ** (-2.0 * i / max(n, 1))
+        if scaling == "linear":
+            w = w / factor
+        elif scaling == "yarn":
+            if theta == 1.0:
+                raise ValueError("yarn needs theta other than 1")
+            at = [n * math.log(original_length / (2 * math.pi * r)) / (2 * math.log(theta))
+                  for r in (fast_turns, slow_turns)]
+            low, high = max(0, math.floor(at[0])), min(n - 1, math.ceil(at[1]))
+            slow = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+            w = w / factor * slow + w * (1 - slow)
+            scale = 0.1 * math.log(factor) + 1.0
+        freqs.append(w)
+    return torch.cat(freqs).to("cuda" if device is None else device), scale
+
+
+def _rotary_tensor(x, y):
+    xs, ys = x.stride(), y.stride()
+    return RotaryTensor(x.data_ptr(), y.data_ptr(), x.shape[2], _I64x3(xs[0], xs[1], xs[2]),
+                        _I64x3(ys[0], ys[1], ys[2]))
+
+
+def rotary(q, k, pos, freqs, split: Optional[Sequence[int]] = None, layout: str = "interleaved", parts: int = 1,
+           scale: float = 1.0, inverse: bool = False, out=None, stream=None):
+    """Rotary embedding of q [B, S, H, d] and k [B, S, H_k, d] (or None) in one
+    launch (jattn_rotary): bf16, fp16 or fp32, any strides with contiguous
+    channels (a view of the fused projection; ``x.transpose(1, 2)`` of a
+    head-major tensor).
+
+    pos: int32 [S] or [B, S]; with ``split`` (channels of the t, row and col
+    axes) [S, 3] or [B, S, 3].  freqs: fp64 [rot / 2] on the device
+    (rotary_freqs); the first rot channels of each of the ``parts`` equal
+    parts of a head turn, the others are copied.  ``scale`` multiplies the
+    rotated channels.  ``inverse`` applies the transposed map: the gradient
+    of the inputs from that of the outputs.
+    out: (q_out, k_out) of the inputs' shapes and any strides, which may be
+    the inputs themselves; new contiguous tensors when None.
+    Returns (q_out, k_out)."""
+    lib = load()
+    dev = _cuda_device(q, "q")
+    xs = (q,) if k is None else (q, k)
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, S, H, d], got {tuple(q.shape)}")
+    B, S, _, d = q.shape
+    dtype = q.dtype
+    if dtype not in _FLOAT_CODE:
+        raise ValueError(f"q must be bf16, fp16 or fp32, got {dtype}")
+    for name, t in zip(("q", "k"), xs):
+        if t.dim() != 4 or t.shape[0] != B or t.shape[1] != S or t.shape[3] != d:
+            raise ValueError(f"{name} must be [{B}, {S}, H, {d}], got {tuple(t.shape)}")
+        if t.dtype != dtype or t.device != dev:
+            raise ValueError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name}'s channels must be contiguous")
+    if layout not in _ROTARY_LAYOUT:
+        raise ValueError(f"unknown layout {layout!r}")
+    if pos.dtype != torch.int32 or pos.device != dev or not pos.is_contiguous():
+        raise ValueError(f"pos must be a contiguous int32 tensor on {dev}")
+    want = (S,) if split is None else (S, 3)
+    if tuple(pos.shape) == (B, *want):
+        per_batch = pos[0].numel() if B > 1 else 0
+    elif tuple(pos.shape) == want:
+        per_batch = 0
+    else:
+        raise ValueError(f"pos must be {want} or {(B, *want)}, got {tuple(pos.shape)}")
+    if freqs.dtype != torch.float64 or freqs.device != dev or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError(f"freqs must be a contiguous fp64 [rot / 2] tensor on {dev}")
+    if out is not None:
+        if len(out) < len(xs):
+            raise ValueError("out must hold a tensor for q and one for k")
+        for name, x, y in zip(("q", "k"), xs, out):
+            if y.shape != x.shape or y.dtype != dtype or y.device != dev or (x.numel() and y.stride(3) != 1):
+                raise ValueError(f"out for {name} must be {tuple(x.shape)} {dtype} on {dev}, channels contiguous")
+            if x.data_ptr() == y.data_ptr() and x.stride() != y.stride():
+                raise ValueError(f"out for {name} lies over it with other strides")
+    sp = None if split is None else (ctypes.c_int32 * 3)(*[int(n) for n in split])
+
+    def call(st):
+        ys = tuple(torch.empty(x.shape, dtype=dtype, device=dev) for x in xs) if out is None else out
+        ts = (RotaryTensor * len(xs))(*[_rotary_tensor(x, y) for x, y in zip(xs, ys)])
+        _check(lib.jattn_rotary(ts, len(xs), _FLOAT_CODE[dtype], B, S, d, parts, 2 * freqs.numel(), pos.data_ptr(),
+                                per_batch, sp, freqs.data_ptr(), _ROTARY_LAYOUT[layout], scale, inverse, st),
+               "jattn_rotary")
+        return (ys[0], ys[1] if k is not None else None)
+    return _enqueue(dev, stream, (*xs, pos, freqs), call)
+
+
+def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtype=None, stream=None):
+    """act(x w^T + bias) + residual (jattn_linear): x [..., K], w [N, K] of one
+    16-bit type, bias [N] (any float type), residual [..., N] of the output's
+    type; sums and epilogue in fp32.  act: none, gelu, gelu_tanh, silu, relu.
+
+    Output [..., N] of ``out_dtype`` (bf16, fp16 or fp32; x's type unless
+    given), or written to ``out``, which may be ``residual`` itself.  The last
+    dimension must be contiguous and the leading ones one row range; rows
+    whose stride and address are multiples of 16 bytes are the fast case."""
+    lib = load()
+    dev = _cuda_device(x, "x")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"x must be bf16 or fp16, got {x.dtype}")
+    if x.dim() < 1 or w.dim() != 2 or w.shape[1] != x.shape[-1]:
+        raise ValueError(f"x must be [..., K] and w [N, K], got {tuple(x.shape)} and {tuple(w.shape)}")
+    _on(w, "w", dev, (x.dtype,))
+    if act not in _ACT_CODE:
+        raise ValueError(f"unknown activation {act!r}")
+    N, K = w.shape
+    if out is not None:
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = x.dtype
+    if out_dtype not in _FLOAT_CODE:
+        raise ValueError(f"the output must be bf16, fp16 or fp32, got {out_dtype}")
+    shape = (*x.shape[:-1], N)
+    ldx, ldw = _rows(x, "x"), _rows(w, "w")
+    if bias is not None:
+        _on(bias, "bias", dev, tuple(_FLOAT_CODE))
+        if tuple(bias.shape) != (N,) or (N > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias must be a contiguous [{N}], got {tuple(bias.shape)}")
+    ldr = N
+    if residual is not None:
+        _on(residual, "residual", dev, (out_dtype,))
+        if tuple(residual.shape) != shape:
+            raise ValueError(f"residual must be {shape}, got {tuple(residual.shape)}")
+        ldr = _rows(residual, "residual")
+    ldy = N
+    if out is not None:
+        _on(out, "out", dev, (out_dtype,))
+        if tuple(out.shape) != shape:
+            raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
+        ldy = _rows(out, "out")
+    M = x.numel() // K if K else 0
+
+    def call(st):
+        y = torch.empty(shape, dtype=out_dtype, device=dev) if out is None else out
+        sh = LinearShape(M, N, K, ldx, ldw, ldy, ldr, _FLOAT_CODE[x.dtype], _FLOAT_CODE[out_dtype],
+                         0 if bias is None else _FLOAT_CODE[bias.dtype], _ACT_CODE[act])
+        _check(lib.jattn_linear(ctypes.byref(sh), x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+                                None if residual is None else residual.data_ptr(), y.data_ptr(), st), "jattn_linear")
+        return y
+    return _enqueue(dev, stream, (x, w, bias, residual, out), call)
+
+
+def _rows(t, name: str) -> int:
+    """Row stride of a tensor [..., n] seen as one range of rows."""
+    n = t.shape[-1]
+    if t.is_contiguous():
+        return n
+    if n > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    ld, rows = n, 1                          # rows counted from the inside out
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if rows == 1:
+            ld = stride
+        elif stride != rows * ld:
+            raise ValueError(f"{name}'s leading dimensions must be one range of equally spaced rows")
+        rows *= size
+    return ld
+
+
+def fwd_diff(q, k, v, lam, lambda_init: float, norm_w=None, eps: float = 1e-5, kv_len=None, key_mask=None, o=None,
+             lse=None, want_lse: bool = False, softmax_scale: float = 0.0, workspace=None, stream=None):
+    """Differential attention (jattn_fwd_diff): O = softmax(Q1 K1^T) V -
+    lambda_h softmax(Q2 K2^T) V for q [B, H, S_q, d], k and v [B, H_kv, S_kv, d]
+    (fp16 or bf16, strided, channels contiguous; d 64 or 128, each map takes
+    half of q's and k's channels).
+
+    lam: fp32 [4, H, d / 2], lambda_h = exp(lam0 . lam1) - exp(lam2 . lam3) +
+    lambda_init.  norm_w (fp32 [d]): RMSNorm of every head's output, times
+    norm_w and 1 - lambda_init.  kv_len: int32 [B], the valid keys of each
+    batch entry.  key_mask: bool or uint8 [B, S_kv], nonzero where a key takes
+    part.  Returns (o bf16 [B, S_q, H, d], lse fp32 [2, B, H, S_q] or None)."""
+    lib = load()
+    dev = _cuda_device(q, "q")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"q must be [B, H, S_q, d] and k [B, H_kv, S_kv, d], got {tuple(q.shape)} and {tuple(k.shape)}")
+    B, H, S_q, d = q.shape
+    H_kv, S_kv = k.shape[1], k.shape[2]
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"q must be bf16 or fp16, got {q.dtype}")
+    for name, t, n in (("q", q, q.shape), ("k", k, (B, H_kv, S_kv, d)), ("v", v, (B, H_kv, S_kv, d))):
+        if tuple(t.shape) != tuple(n) or t.dtype != q.dtype or t.device != dev:
+            raise ValueError(f"{name} must be {tuple(n)} {q.dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+        if t.numel() and t.stride(3) != 1:
+            raise ValueError(f"{name}'s channels must be contiguous")
+    for name, t, dtypes, n in (("lam", lam, (torch.float32,), (4, H, d // 2)), ("norm_w", norm_w, (torch.float32,), (d,)),
+                               ("kv_len", kv_len, (torch.int32,), (B,)),
+                               ("key_mask", key_mask, (torch.bool, torch.uint8), (B, S_kv)),
+                               ("o", o, (torch.bfloat16,), (B, S_q, H, d)),
+                               ("lse", lse, (torch.float32,), (2, B, H, S_q))):
+        if t is None:
+            continue
+        _on(t, name, dev, dtypes)
+        if tuple(t.shape) != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {n}, got {tuple(t.shape)}")
+    sh = DiffShape(B, H, H_kv, S_q, S_kv, d, _I64x3(*q.stride()[:3]), _I64x3(*k.stride()[:3]), _I64x3(*v.stride()[:3]))
+    need = lib.jattn_fwd_diff_workspace(ctypes.byref(sh))
+    if workspace is not None:
+        _on(workspace, "workspace", dev, (torch.uint8,))
+        if not workspace.is_contiguous() or workspace.numel() < need:
+            raise ValueError(f"workspace must hold at least {need} contiguous bytes, got {workspace.numel()}")
+
+    def call(st):
+        ws, oo, ll = workspace, o, lse
+        if ws is None and need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        if oo is None:
+            oo = torch.empty(B, S_q, H, d, dtype=torch.bfloat16, device=dev)
+        if ll is None and want_lse:
+            ll = torch.empty(2, B, H, S_q, dtype=torch.float32, device=dev)
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        _check(lib.jattn_fwd_diff(ctypes.byref(sh), _FLOAT_CODE[q.dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                  lam.data_ptr(), lambda_init, ptr(norm_w), eps, ptr(kv_len), ptr(key_mask), ptr(ws),
+                                  0 if ws is None else ws.numel(), oo.data_ptr(), ptr(ll), softmax_scale, st),
+               "jattn_fwd_diff")
+        return oo, ll
+    return _enqueue(dev, stream, (q, k, v, lam, norm_w, kv_len, key_mask, o, lse, workspace), call)
 
 
 def flops(B: int, H: int, S: int, d: int) -> int:

@@ -63,7 +63,8 @@ typedef enum {
 #define JATTN_DEV_RANGE 2u
 #define JATTN_DEV_CHECK 4u
 
-typedef enum { JATTN_BF16 = 0, JATTN_FP16 = 1, JATTN_E4M3 = 2 } jattn_dtype;
+/* JATTN_FP32 only where an entry point says so. */
+typedef enum { JATTN_BF16 = 0, JATTN_FP16 = 1, JATTN_E4M3 = 2, JATTN_FP32 = 3 } jattn_dtype;
 
 /* Problem shape.  S = S_txt + S_img + S_ref in [1, 2^24], each part >= 0;
  * B, H >= 1 with B * H <= 65535 and ceil(S / 256) * B * H < 2^31; d in
@@ -351,6 +352,136 @@ jattn_status jattn_joint_attention_host(const jattn_shape* shape, const void* qk
                                         const void* qkv_ref, const int32_t* pos, float theta,
                                         const int32_t split[3], jattn_dtype path, void* o, float softmax_scale,
                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The layer around the attention.  ("Speed Up Image Generation with FLUX 3
+ * Image Klein on NVIDIA Blackwell GPUs", section "GEMM kernel optimization":
+ * projections with fused epilogues and RoPE before the attention; the forms
+ * below are this library's own.)  The three entry points that follow take
+ * strides, so that a projection's output is read where it lies.
+ */
+
+/* Pairs of the rotary embedding: channels (2i, 2i + 1), or (i, i + rot / 2). */
+typedef enum { JATTN_ROTARY_INTERLEAVED = 0, JATTN_ROTARY_HALF = 1 } jattn_rotary_layout;
+
+/* One tensor to rotate: x [B, S, H, d] -> y, strides in elements over (batch
+ * entry, token, head); the d channels of a head are contiguous.  y may be x
+ * with the same strides; otherwise the two must not overlap, and y must not
+ * overlap itself.  Pointers aligned to their element; 16-byte aligned ones
+ * with strides of whole 16 bytes are moved 16 bytes at a time. */
+typedef struct {
+  const void* x;
+  void* y;
+  int32_t H;
+  int64_t x_stride[3], y_stride[3];
+} jattn_rotary_tensor;
+
+/*
+ * Rotary embedding of one or two tensors (queries and keys, whose head counts
+ * may differ) in one launch:
+ *   (a, b) -> scale * (a cos t - b sin t, a sin t + b cos t),
+ *   t = pos * freqs[pair] formed in fp64, the products in fp32, one rounding.
+ * The channels of a head are `parts` equal parts (the two maps of
+ * differential attention), each rotated by itself: its first rot channels
+ * (even, in [2, d / parts]; d / parts even) turn, the others are copied.
+ *   tensors   : host array of n_tensors (1 or 2).
+ *   dtype     : JATTN_BF16, JATTN_FP16 or JATTN_FP32, input and output.
+ *   pos       : int32 [B or 1][S][n_axes], n_axes = split ? 3 : 1;
+ *               pos_stride_b elements between batch entries, 0 if shared.
+ *   split     : NULL, or a host array of 3 even, non-negative channel counts
+ *               that sum to rot: the pairs of the t, row and col axes, in
+ *               that order.
+ *   freqs     : device fp64 [rot / 2], radians per position.
+ *   scale     : factor of the rotated channels (1, or the attention factor of
+ *               a long-context scaling), finite.
+ *   inverse   : 0, or nonzero for the transposed map (turned by -t): the
+ *               gradient with respect to x is the inverse of that of y.
+ * Errors: JATTN_ERR_INVALID_ARG, JATTN_ERR_UNSUPPORTED (dtype),
+ * JATTN_ERR_ALIGNMENT.  B or S or every H of 0 is no work and JATTN_OK.
+ */
+jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors, jattn_dtype dtype, int32_t B,
+                          int32_t S, int32_t d, int32_t parts, int32_t rot, const int32_t* pos,
+                          int64_t pos_stride_b, const int32_t* split, const double* freqs,
+                          jattn_rotary_layout layout, float scale, int32_t inverse, void* stream);
+
+/* Activation of the linear layer: none, x Phi(x), its tanh form, x sigmoid(x),
+ * max(x, 0). */
+typedef enum {
+  JATTN_ACT_NONE = 0,
+  JATTN_ACT_GELU = 1,
+  JATTN_ACT_GELU_TANH = 2,
+  JATTN_ACT_SILU = 3,
+  JATTN_ACT_RELU = 4
+} jattn_act;
+
+/* Row strides ldx, ldw >= K and ldy, ldr >= N in elements.  M, N in [0, 2^31),
+ * K in [1, 2^31). */
+typedef struct {
+  int32_t M, N, K;
+  int64_t ldx, ldw, ldy, ldr;
+  jattn_dtype in_dtype;      /* x, w: JATTN_BF16 or JATTN_FP16 */
+  jattn_dtype out_dtype;     /* y, residual: JATTN_BF16, JATTN_FP16 or JATTN_FP32 */
+  jattn_dtype bias_dtype;    /* JATTN_BF16, JATTN_FP16 or JATTN_FP32 */
+  jattn_act act;
+} jattn_linear_shape;
+
+/*
+ * Linear layer with its epilogue: y = act(x w^T + bias) + residual, sums and
+ * epilogue in fp32, one rounding.
+ *   x [M][K], w [N][K] : in_dtype;  bias [N] or NULL;  residual [M][N] or
+ *   NULL (may be y itself, with ldr == ldy; y overlaps nothing else).
+ * Any sizes and strides; x and w whose pointers and row strides are multiples
+ * of 16 bytes are moved by TMA, others by element loads (slower).  No
+ * workspace; the same call gives the same bits every time.
+ * Errors: JATTN_ERR_INVALID_ARG, JATTN_ERR_UNSUPPORTED (types, act),
+ * JATTN_ERR_ALIGNMENT (a pointer not aligned to its element).  M or N of 0 is
+ * no work and JATTN_OK.
+ */
+jattn_status jattn_linear(const jattn_linear_shape* shape, const void* x, const void* w, const void* bias,
+                          const void* residual, void* y, void* stream);
+
+/* Differential attention's shape.  Strides in elements over (batch entry,
+ * head, token), multiples of 8; channels contiguous.  d in {64, 128};
+ * H_kv >= 1 divides H; B, S_q, S_kv >= 0 (S_kv 0: every row is empty),
+ * S_q, S_kv <= 2^24, B * H <= 65535. */
+typedef struct {
+  int32_t B, H, H_kv, S_q, S_kv, d;
+  int64_t q_stride[3], k_stride[3], v_stride[3];
+} jattn_diff_shape;
+
+/*
+ * Differential attention forward, 16-bit operands:
+ *   A_m = softmax(Q_m K_m^T * softmax_scale), m = 1, 2, over the allowed keys,
+ *   Q = [Q_1 | Q_2], K = [K_1 | K_2] with d / 2 channels each, V with d;
+ *   O = A_1 V - lambda_h A_2 V,
+ *   lambda_h = exp(a_1 . b_1) - exp(a_2 . b_2) + lambda_init,
+ * and with norm_w, per (token, head), O <- w * O / sqrt(mean(O^2) + eps) *
+ * (1 - lambda_init).
+ *   q [B, H, S_q, d], k and v [B, H_kv, S_kv, d] : in_dtype (JATTN_BF16 or
+ *              JATTN_FP16), strided; query head h reads K/V head
+ *              h / (H / H_kv).  S_q = 1 is the single-token form.
+ *   lam      : fp32 [4][H][d / 2]: a_1, b_1, a_2, b_2 of every head.
+ *   norm_w   : fp32 [d], or NULL for no norm; eps > 0 with it.
+ *   kv_len   : int32 [B] or NULL: batch entry b has the first
+ *              kv_len[b] keys of its S_kv (clamped into [0, S_kv]).
+ *   key_mask : uint8 [B][S_kv] or NULL: keys with 0 take no part (padded text
+ *              inside the joint sequence).  Whatever lies in masked keys'
+ *              rows of k and v (NaN, infinities) has no effect.
+ *   o        : bf16 [B, S_q, H, d] contiguous.  A row without a key is zeros.
+ *   lse      : fp32 [2][B][H][S_q], the natural-log sum-exp of both maps
+ *              (-inf for a row without a key), or NULL.
+ *   softmax_scale <= 0 selects 1 / sqrt(d / 2).
+ *   workspace: device scratch of at least jattn_fwd_diff_workspace(shape)
+ *              bytes, 256-byte aligned (NULL where that is 0).  Calls that
+ *              may overlap on the GPU need one each.
+ * Pointers 16-byte aligned (kv_len, lse 4; key_mask 1).  Errors as
+ * jattn_fwd_bf16.  B or S_q of 0 is no work and JATTN_OK.
+ */
+size_t jattn_fwd_diff_workspace(const jattn_diff_shape* shape);   /* 0: none needed, or invalid arguments */
+jattn_status jattn_fwd_diff(const jattn_diff_shape* shape, jattn_dtype in_dtype, const void* q, const void* k,
+                            const void* v, const float* lam, float lambda_init, const float* norm_w, float eps,
+                            const int32_t* kv_len, const uint8_t* key_mask, void* workspace,
+                            size_t workspace_bytes, void* o, float* lse, float softmax_scale, void* stream);
 
 /*
  * The boundary's status query: wait for the work enqueued on `stream` so far,

@@ -1,0 +1,197 @@
+"""Differential attention against the fp64 oracle.
+
+Tolerance per element: half a step of the bf16 output, plus the oracle's
+first-order bound for probabilities that are off by u = half a step of the
+operand type (P is rounded to it) + 2^-13 (the fp32 logits: d / 2 products of
+up to 2^-23 of sum |q k| each, 64 * 2^-23 * 64 * scale at most, and exp2's
+2^-22), twice for the terms of second order.  The log-sum-exp moves by 2^-13."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.layer as ref
+from diffusion_transformer_joint_jattn_b200 import jattn
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+INIT, EPS = 0.35, 1e-5
+
+
+def make(dev, dtype, B, H, H_kv, S_q, S_kv, d, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    mk = lambda h, s: torch.randn(B, h, s, d, generator=g).to(DT[dtype]).to(dev)  # noqa: E731
+    lam = (0.2 * torch.randn(4, H, d // 2, generator=g)).to(dev)
+    return mk(H, S_q), mk(H_kv, S_kv), mk(H_kv, S_kv), lam, (1 + 0.1 * torch.randn(d, generator=g)).to(dev)
+
+
+def check(o, lse, q, k, v, lam, w, allowed=None, scale=None):
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    u = torch.finfo(q.dtype).eps / 2 + 2.0 ** -13
+    want, lref, bound = ref.diff_attention(f(q), f(k), f(v), f(lam), INIT, None if w is None else f(w), EPS, allowed,
+                                           scale, u)
+    err = np.abs(f(o) - want)
+    tol = 2.0 ** -8 * np.abs(want) + 2 * bound + 1e-6
+    assert (err <= tol).all(), float((err / tol).max())
+    if lse is not None:
+        l = f(lse)
+        assert (np.isneginf(l) == np.isneginf(lref)).all()
+        live = np.isfinite(lref)
+        assert np.abs(l[live] - lref[live]).max(initial=0.0) <= 2.0 ** -13
+    assert jattn.device_status()[0] == jattn.OK
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,H_kv,S_q,S_kv", [
+    (1, 1, 1, 1, 1), (1, 2, 2, 288, 288), (2, 4, 2, 1, 700), (3, 6, 2, 5, 129), (1, 3, 1, 130, 127), (2, 2, 1, 257, 385),
+    (1, 4, 4, 1, 5000), (1, 8, 1, 16, 4100), (1, 2, 2, 64, 1),
+])
+def test_sizes(cuda_device, dtype, d, B, H, H_kv, S_q, S_kv):
+    q, k, v, lam, w = make(cuda_device, dtype, B, H, H_kv, S_q, S_kv, d)
+    for norm in (w, None):
+        o, lse = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=norm, eps=EPS, want_lse=True)
+        check(o, lse, q, k, v, lam, norm)
+
+
+@pytest.mark.parametrize("S_q,S_kv", [(1, 3000), (40, 3000), (150, 300)])
+def test_lengths(cuda_device, S_q, S_kv):
+    """Lengths of 0, 1, inside a tile, at its end, all, and past the cache; the
+    rest of the cache holds NaN and infinities."""
+    lens = [0, 1, 100, 128, 129, S_kv - 1, S_kv, S_kv + 50]
+    q, k, v, lam, w = make(cuda_device, "bf16", len(lens), 4, 2, S_q, S_kv, 128)
+    allowed = np.arange(S_kv)[None] < np.array(lens)[:, None]
+    for b, n in enumerate(lens):
+        k[b, :, n:] = float("nan")
+        v[b, :, n:] = float("inf")
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    o, lse = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, eps=EPS, kv_len=n, want_lse=True)
+    clean = lambda t: torch.where(torch.from_numpy(allowed).to(t.device)[:, None, :, None], t, 0)  # noqa: E731
+    check(o, lse, q, clean(k), clean(v), lam, w, allowed)
+    assert (o[0] == 0).all() and torch.isneginf(lse[:, 0]).all()
+
+
+@pytest.mark.parametrize("S_q", [1, 200])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.0e38])
+def test_key_mask(cuda_device, S_q, bad):
+    """Padded text inside the joint sequence, whole masked tiles, scattered
+    keys, a single key, none; masked rows of k and v hold what they like."""
+    S = 900
+    q, k, v, lam, w = make(cuda_device, "bf16", 5, 2, 2, S_q, S, 128, seed=1)
+    allowed = np.ones((5, S), bool)
+    allowed[0, 40:512] = False
+    allowed[1] = np.random.default_rng(0).random(S) < 0.5
+    allowed[2] = False
+    allowed[2, 700] = True
+    allowed[3] = False
+    m = torch.from_numpy(allowed).to(cuda_device)
+    kk, vv = (torch.where(m[:, None, :, None], t, torch.full_like(t, bad)) for t in (k, v))
+    n = torch.tensor([900, 830, 900, 900, 384], dtype=torch.int32, device=cuda_device)
+    both = allowed & (np.arange(S)[None] < n.cpu().numpy()[:, None])
+    zero = lambda t: torch.where(torch.from_numpy(both).to(t.device)[:, None, :, None], t, 0)  # noqa: E731
+    for mask in (m, m.to(torch.uint8) * 255):
+        o, lse = jattn.fwd_diff(q, kk, vv, lam, INIT, norm_w=w, eps=EPS, kv_len=n, key_mask=mask, want_lse=True)
+        check(o, lse, q, zero(k), zero(v), lam, w, both)
+        assert (o[3] == 0).all()
+
+
+def test_split_and_whole_walk_agree(cuda_device):
+    """The same queries alone (keys split over CTAs) and among enough others to
+    fill the GPU (one walk): within both forms' rounding of the output."""
+    q, k, v, lam, w = make(cuda_device, "fp16", 1, 2, 2, 128 * 80, 2048, 128)
+    a, la = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, eps=EPS, want_lse=True)
+    b, lb = jattn.fwd_diff(q[:, :, :100], k, v, lam, INIT, norm_w=w, eps=EPS, want_lse=True)
+    assert torch.allclose(a[:, :100].float(), b.float(), rtol=2 * 2.0 ** -8, atol=4 * 2.0 ** -11)
+    assert torch.allclose(la[..., :100], lb, rtol=0, atol=2.0 ** -13)
+
+
+def test_strided_operands(cuda_device):
+    """q, k and v as views of a fused [B, S, 3, H, d] projection, and a query
+    tensor whose shared heads' rows are not equally spaced."""
+    B, S, H, d = 2, 150, 4, 128
+    qkv = torch.randn(B, S, 3, H, d, generator=torch.Generator().manual_seed(4)).to(torch.bfloat16).to(cuda_device)
+    q, k, v = (qkv[:, :, i].transpose(1, 2) for i in range(3))
+    _, _, _, lam, w = make(cuda_device, "bf16", B, H, H, 1, 1, d)
+    o, lse = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, eps=EPS, want_lse=True)
+    same, _ = jattn.fwd_diff(q.contiguous(), k.contiguous(), v.contiguous(), lam, INIT, norm_w=w, eps=EPS)
+    assert torch.equal(o, same)
+    check(o, lse, q, k, v, lam, w)
+    shared, _ = jattn.fwd_diff(q, k[:, :2], v[:, :2], lam, INIT, norm_w=w, eps=EPS)
+    check(shared, None, q, k[:, :2], v[:, :2], lam, w)
+    packed, _ = jattn.fwd_diff(q.contiguous(), k[:, :2], v[:, :2], lam, INIT, norm_w=w, eps=EPS)
+    assert torch.equal(shared, packed)
+
+
+def test_large_logits_and_scale(cuda_device):
+    """Logits of hundreds: the running maximum moves far between tiles, and the
+    softmax picks single keys.  fp32 logits of size L are off by 64 * 2^-23 of
+    their magnitudes; at scale 1 and |q k| sums of up to 4000 that is 2^-5."""
+    q, k, v, lam, _ = make(cuda_device, "fp16", 1, 2, 2, 130, 600, 128, seed=5)
+    for t in (q, k):
+        t.mul_(2)
+    o, lse = jattn.fwd_diff(q, k, v, lam, INIT, want_lse=True, softmax_scale=1.0)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    want, lref, _ = ref.diff_attention(f(q), f(k), f(v), f(lam), INIT, scale=1.0)
+    assert np.abs(f(lse) - lref).max() <= 2.0 ** -5
+    assert np.linalg.norm(f(o) - want) <= (2.0 ** -8 + 2.0 ** -5) * np.linalg.norm(want)
+
+
+def test_no_keys_and_no_queries(cuda_device):
+    q, k, v, lam, w = make(cuda_device, "bf16", 2, 2, 1, 3, 4, 64)
+    o, lse = jattn.fwd_diff(q, k[:, :, :0], v[:, :, :0], lam, INIT, norm_w=w, want_lse=True)
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = jattn.fwd_diff(q[:, :, :0], k, v, lam, INIT, want_lse=True)
+    assert o.shape == (2, 0, 2, 64) and lse.shape == (2, 2, 2, 0)
+    assert jattn.fwd_diff(q[:0], k[:0], v[:0], lam, INIT)[0].shape == (0, 3, 2, 64)
+
+
+def test_outputs_in_place_and_what_surrounds_them(cuda_device):
+    q, k, v, lam, w = make(cuda_device, "bf16", 1, 3, 1, 70, 200, 64)
+    buf = torch.full((70 * 3 * 64 + 64,), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    o = buf[8:8 + 70 * 192].view(1, 70, 3, 64)                 # 16-byte, not 32-byte aligned
+    lse = torch.full((2, 1, 3, 70), 7.0, device=cuda_device)
+    got, l = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, eps=EPS, o=o, lse=lse)
+    assert got is o and l is lse
+    check(o, lse, q, k, v, lam, w)
+    assert (buf[:8] == 7).all() and (buf[8 + 70 * 192:] == 7).all()
+
+
+def test_refusals(cuda_device):
+    q, k, v, lam, w = make(cuda_device, "bf16", 2, 4, 2, 3, 9, 128)
+    ok = dict(q=q, k=k, v=v, lam=lam, lambda_init=INIT, norm_w=w)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    for bad in (dict(q=q.cpu()), dict(q=q.float()), dict(k=k.half()), dict(v=v[:, :, :4]), dict(q=q[0]),
+                dict(lam=lam[:3]), dict(lam=lam.cpu()), dict(norm_w=w[:64]), dict(kv_len=i32(3)),
+                dict(kv_len=i32(2).long()), dict(key_mask=i32(2, 9)), dict(key_mask=i32(2, 8).bool()),
+                dict(o=torch.empty(2, 3, 4, 128, device=cuda_device)), dict(lse=torch.empty(2, 4, 3, device=cuda_device)),
+                dict(q=q.transpose(2, 3).contiguous().transpose(2, 3))):
+        with pytest.raises(ValueError):
+            jattn.fwd_diff(**dict(ok, **bad))
+    for bad in (dict(eps=0.0), dict(lambda_init=float("inf")), dict(softmax_scale=float("nan")),
+                dict(q=q[:, :3], lam=lam[:, :3].contiguous()), dict(k=k[:, :1].expand(2, 2, 9, 128), v=v)):
+        with pytest.raises(jattn.JattnError):
+            jattn.fwd_diff(**dict(ok, **bad))
+    q1, k1, v1, lam1, _ = make(cuda_device, "bf16", 1, 1, 1, 1, 4096, 128)
+    with pytest.raises(ValueError):
+        jattn.fwd_diff(q1, k1, v1, lam1, INIT, workspace=torch.empty(16, dtype=torch.uint8, device=cuda_device))
+
+
+def test_other_stream_and_graph(cuda_device):
+    for S_q in (1, 300):
+        q, k, v, lam, w = make(cuda_device, "bf16", 1, 4, 2, S_q, 3000, 128)
+        want, _ = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got, _ = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want)
+        graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+        outs = []
+        for g in graphs:
+            with torch.cuda.graph(g):
+                outs.append(jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w)[0])
+        q.neg_()
+        for g in graphs:
+            g.replay()
+        want, _ = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w)
+        assert all(torch.equal(o, want) for o in outs)

@@ -1,0 +1,149 @@
+"""The linear layer with its epilogue against the fp64 oracle.
+
+Tolerance per element: half a step of the output type of the result, plus the
+fp32 sum: K products (exact in fp32) added with at most one unit of 2^-23 of
+the sum of magnitudes each, scaled by the activation's slope (at most 1.13),
+plus 2^-18 of the result for the epilogue's approximate exp and reciprocal."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.layer as ref
+from diffusion_transformer_joint_jattn_b200 import jattn
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def make(dev, dtype, M, N, K, seed=0, out=None, bias="same", residual=False):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K, generator=g).to(DT[dtype]).to(dev)
+    w = (torch.randn(N, K, generator=g) / K ** 0.5).to(DT[dtype]).to(dev)
+    b = None if bias is None else torch.randn(N, generator=g).to(DT[dtype if bias == "same" else bias]).to(dev)
+    r = torch.randn(M, N, generator=g).to(DT[out or dtype]).to(dev) if residual else None
+    return x, w, b, r
+
+
+def check(y, x, w, b, act, r):
+    f = lambda t: None if t is None else t.double().cpu().numpy()  # noqa: E731
+    want = ref.linear(f(x), f(w), f(b), act, f(r))
+    sums = np.abs(f(x)) @ np.abs(f(w)).T + (0 if b is None else np.abs(f(b)))
+    tol = (torch.finfo(y.dtype).eps / 2 + 2.0 ** -18) * np.abs(want) + 1.13 * (x.shape[1] + 2) * 2.0 ** -23 * sums
+    if r is not None:
+        tol += 2.0 ** -18 * np.abs(f(r))
+    err = np.abs(y.double().cpu().numpy() - want)
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+SIZES = [
+    (1, 128, 64), (1, 1, 1), (3, 257, 512), (16, 1000, 2048), (17, 128, 96), (33, 300, 1000), (64, 64, 4096),
+    (65, 65, 65), (127, 255, 63), (128, 128, 128), (129, 640, 72), (300, 777, 1003), (512, 2048, 512),
+    (1000, 1500, 333), (2304, 2304, 192), (2500, 2700, 264),
+]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("fp16", "fp32")])
+def test_sizes(cuda_device, M, N, K, dtype, out):
+    x, w, b, r = make(cuda_device, dtype, M, N, K, out=out, residual=True)
+    y = jattn.linear(x, w, b, residual=r, out_dtype=DT[out])
+    assert y.shape == (M, N) and y.dtype == DT[out]
+    check(y, x, w, b, "none", r)
+    assert jattn.device_status()[0] == jattn.OK
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "gelu_tanh", "silu", "relu"])
+@pytest.mark.parametrize("M", [5, 200, 2304])
+@pytest.mark.parametrize("dtype,out,bias", [("bf16", "fp32", "fp32"), ("fp16", "fp16", "same"), ("bf16", "fp16", None)])
+def test_epilogues(cuda_device, act, M, dtype, out, bias):
+    N, K = (2304, 128) if M > 1000 else (200, 128)
+    x, w, b, _ = make(cuda_device, dtype, M, N, K, seed=M, out=out, bias=bias)
+    y = jattn.linear(4 * x, w, b, act=act, out_dtype=DT[out])
+    check(y, 4 * x, w, b, act, None)
+
+
+@pytest.mark.parametrize("M,N,K", [(7, 129, 200), (150, 140, 130), (2304, 2310, 136)])
+def test_strides(cuda_device, M, N, K):
+    """Rows inside wider buffers, aligned for TMA or not, on both sides; what
+    lies around the output is left as it was."""
+    x0, w0, b, r0 = make(cuda_device, "bf16", M, N, K, residual=True)
+    for pad, off in ((8, 8), (3, 1)):
+        big = lambda t: torch.zeros(t.shape[0], t.shape[1] + pad + off, dtype=t.dtype, device=cuda_device)  # noqa: E731
+        views = []
+        for t in (x0, w0, r0):
+            v = big(t)[:, off:off + t.shape[1]]
+            v.copy_(t)
+            views.append(v)
+        x, w, r = views
+        out = torch.full((M + 2, N + 40), 7.0, dtype=torch.bfloat16, device=cuda_device)
+        y = jattn.linear(x, w, b, residual=r, out=out[1:-1, off:off + N])
+        check(y, x0, w0, b, "none", r0)
+        y.fill_(7.0)
+        assert (out == 7.0).all()
+
+
+def test_residual_in_place_and_leading_dimensions(cuda_device):
+    x, w, b, _ = make(cuda_device, "bf16", 6 * 50, 320, 96)
+    r = torch.randn(6, 50, 320, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).to(cuda_device)
+    want = jattn.linear(x.view(6, 50, 96), w, b, "silu", residual=r)
+    assert want.shape == (6, 50, 320)
+    got = r.clone()
+    assert jattn.linear(x.view(6, 50, 96), w, b, "silu", residual=got, out=got) is got
+    assert torch.equal(got, want)
+    check(want.view(300, 320), x, w, b, "silu", r.view(300, 320))
+
+
+def test_infinities_stay_in_their_rows(cuda_device):
+    for M, N, K in ((20, 300, 200), (300, 300, 200), (2304, 2304, 136)):
+        x, w, b, _ = make(cuda_device, "bf16", M, N, K)
+        clean = jattn.linear(x, w, b)
+        x[M // 2, 3] = float("inf")
+        w[7, 5] = float("nan")
+        y = jattn.linear(x, w, b)
+        assert torch.isnan(y[:, 7]).all() and not torch.isfinite(y[M // 2]).any()
+        keep = torch.ones_like(y, dtype=torch.bool)
+        keep[:, 7] = keep[M // 2] = False
+        assert torch.equal(y[keep], clean[keep])
+
+
+def test_same_bits_every_time(cuda_device):
+    for M, N, K in ((4, 512, 4096), (100, 256, 2048), (2500, 2700, 264)):
+        x, w, b, _ = make(cuda_device, "fp16", M, N, K)
+        first = jattn.linear(x, w, b, "gelu")
+        assert all(torch.equal(first, jattn.linear(x, w, b, "gelu")) for _ in range(3))
+
+
+def test_nothing_to_do(cuda_device):
+    w = torch.zeros(8, 16, dtype=torch.bfloat16, device=cuda_device)
+    assert jattn.linear(torch.zeros(0, 16, dtype=torch.bfloat16, device=cuda_device), w).shape == (0, 8)
+    assert jattn.linear(torch.zeros(3, 16, dtype=torch.bfloat16, device=cuda_device), w[:0]).shape == (3, 0)
+
+
+def test_refusals(cuda_device):
+    x, w, b, r = make(cuda_device, "bf16", 6, 8, 16, residual=True)
+    for bad in (dict(x=x.cpu()), dict(x=x.float()), dict(w=w.half()), dict(w=w[:, :8]), dict(act="swish"),
+                dict(bias=b[:4]), dict(bias=b.cpu()), dict(residual=r.float()), dict(residual=r[:3]),
+                dict(out=torch.empty(6, 9, dtype=torch.bfloat16, device=cuda_device)), dict(out_dtype=torch.int32),
+                dict(x=x.t().contiguous().t()), dict(x=torch.stack([x, x], 1)[:4:2].transpose(0, 1))):
+        with pytest.raises(ValueError):
+            jattn.linear(**dict(dict(x=x, w=w, bias=b, residual=r), **bad))
+    with pytest.raises(jattn.JattnError):
+        jattn.linear(x[:, :0], w[:, :0])
+
+
+def test_other_stream_and_graph(cuda_device):
+    for M, N, K in ((4, 256, 1024), (2304, 2304, 128)):
+        x, w, b, _ = make(cuda_device, "bf16", M, N, K)
+        want = jattn.linear(x, w, b)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = jattn.linear(x, w, b, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got, want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = jattn.linear(x, w, b)
+        x.neg_()
+        graph.replay()
+        assert torch.equal(y, jattn.linear(x, w, b))
