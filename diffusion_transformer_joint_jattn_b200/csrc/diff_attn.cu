@@ -146,6 +146,57 @@ __device__ __forceinline__ int key_count(const DiffParams& p, int b) {
   return p.kv_len != nullptr ? min(max(__ldg(p.kv_len + b), 0), p.S_kv) : p.S_kv;
 }
 
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+// Exponent e of the power of two that V is divided by before it is rounded to
+// fp16, from the bits of its largest finite magnitude: brings that into
+// [2^14, 2^15), so that values down to 2^-29 of it keep all their bits.
+// Clamped so that 2^e and 2^-e are normal fp32 numbers.
+__device__ __forceinline__ int v_exponent(uint32_t amax_bits) {
+  return amax_bits == 0u ? 0 : min(max(static_cast<int>(amax_bits >> 23) - 127 - 14, -126), 126);
+}
+
+// V's largest finite magnitude per (batch entry, K/V head) over its allowed
+// keys, then its fp16 copy, zeros at masked keys: 8 channels of a row per
+// thread and step, blockIdx.y = the head, kConvRows rows per block.
+constexpr int kConvRows = 128;
+template <int D, bool CONVERT>
+__global__ void __launch_bounds__(256) widen_v_kernel(const DiffParams p) {
+  constexpr int TPR = D / 8;
+  const int bh = blockIdx.y, b = bh / p.H_kv, h = bh % p.H_kv;
+  const int len = key_count(p, b);
+  const int c = threadIdx.x % TPR * 8;
+  const __nv_bfloat16* v = p.v + b * p.v_stride[0] + h * p.v_stride[1] + c;
+  const float f = CONVERT ? pow2(-v_exponent(p.v_amax[bh])) : 1.f;
+  uint32_t most = 0u;
+#pragma unroll 4
+  for (int i = threadIdx.x / TPR; i < kConvRows; i += 256 / TPR) {
+    const int s = blockIdx.x * kConvRows + i;
+    if (s >= p.S_kv) break;
+    const bool in = s < len && (p.key_mask == nullptr || __ldg(p.key_mask + static_cast<size_t>(b) * p.S_kv + s) != 0);
+    uint4 x = make_uint4(0u, 0u, 0u, 0u);
+    if (in) x = __ldg(reinterpret_cast<const uint4*>(v + static_cast<int64_t>(s) * p.v_stride[2]));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if constexpr (CONVERT) {
+      uint32_t y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        y[j] = pack_x2<false>(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xFFFF0000u) * f);
+      *reinterpret_cast<uint4*>(p.v16 + (static_cast<size_t>(bh) * p.S_kv + s) * D + c) = make_uint4(y[0], y[1], y[2], y[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = (w[j] << 16) & 0x7FFF0000u, hi = w[j] & 0x7FFF0000u;
+        if (lo < 0x7F800000u) most = max(most, lo);
+        if (hi < 0x7F800000u) most = max(most, hi);
+      }
+    }
+  }
+  if constexpr (!CONVERT) {
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((threadIdx.x & 31) == 0 && most != 0u) atomicMax(p.v_amax + bh, most);
+  }
+}
+
 // lambda of one head, fp32 sums of the two dot products.
 __device__ __forceinline__ float lambda_of(const DiffParams& p, int head, int dm) {
   const size_t plane = static_cast<size_t>(p.H) * dm;
@@ -162,12 +213,22 @@ __device__ __forceinline__ float lambda_of(const DiffParams& p, int head, int dm
   return expf(s1) - expf(s2) + p.lambda_init;
 }
 
-template <int D, bool BF16>
+// KIND: the operands' types and how P keeps its precision.  P in bf16 alone
+// costs the output 1.9e-3 (relative, N(0, 1) inputs), more than the bf16
+// output's own rounding, because the difference of the maps cancels.
+enum : int {
+  kF16 = 0,        // fp16 operands, P in fp16
+  kBf16WideV = 1,  // bf16 Q and K; V converted to fp16 (scaled by a power of two per head), P in fp16
+  kBf16Split = 2,  // bf16 operands, P as the sum of two bf16: twice the P.V products, no second copy of V
+};
+
+template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const DiffParams p) {
   using C = Cfg<D>;
   constexpr int DM = D / 2;
+  constexpr bool QK_BF16 = KIND != kF16, PV_BF16 = KIND == kBf16Split;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sQ = smem;
@@ -194,8 +255,9 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const int n_kv = static_cast<int>(static_cast<long long>(n_total) * (sp + 1) / p.splits) - t0;
   const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(b) * p.S_kv : nullptr;
   // V rows of masked keys have to be zeroed: a mask, or a length inside the
-  // cache (rows past the cache arrive as zeros from TMA)
-  const bool fix = mask != nullptr || len < p.S_kv;
+  // cache (rows past the cache arrive as zeros from TMA; the converted V has
+  // its masked rows zeroed)
+  const bool fix = KIND != kBf16WideV && (mask != nullptr || len < p.S_kv);
 
   if (threadIdx.x == 0) {
     mbar_init(&bar->q_full, 1);
@@ -257,8 +319,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     } else if (warp == kMmaWarp) {
       if (lane == 0 && n_kv > 0) {
-        const uint32_t idesc_qk = instr_desc(BF16, BF16, 0, BM, BN);
-        const uint32_t idesc_pv = instr_desc(BF16, BF16, 1, BM, D);
+        const uint32_t idesc_qk = instr_desc(QK_BF16, QK_BF16, 0, BM, BN);
+        const uint32_t idesc_pv = instr_desc(PV_BF16, PV_BF16, 1, BM, D);
         const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
         bool any_mma = false;
         auto issue_qk = [&](int t, int ks) {
@@ -276,6 +338,12 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int kk = 0; kk < BN / 16; ++kk)
             mma_f16_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8,
                        smem_desc(sVa + vs * C::TB + kk * 16 * 128, C::BOXB, 1024, 2u), idesc_pv, acc || kk > 0);
+          if constexpr (KIND == kBf16Split) {
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)               // the low parts, in the columns behind
+              mma_f16_ts(tmem + col_o(t), tmem + col_s(t) + 64 + kk * 8,
+                         smem_desc(sVa + vs * C::TB + kk * 16 * 128, C::BOXB, 1024, 2u), idesc_pv, 1);
+          }
         };
         bool ok = mbar_wait(&bar->q_full, 0, ctl) && mbar_wait(&bar->k_full[0], 0, ctl);
         if (ok) {
@@ -428,7 +496,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
+        uint32_t pk[32], lo[KIND == kBf16Split ? 32 : 1];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
           const int e = half * 64 + 2 * c;
@@ -438,12 +506,17 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const float2 e1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
           acc0 = __fadd2_rn(acc0, e0);
           acc1 = __fadd2_rn(acc1, e1);
-          // P in the operands' type (the MMA wants one type); l sums the
-          // unrounded values, so the rounding stays unbiased
-          pk[c] = pack_x2<BF16>(e0.x, e0.y);
-          pk[c + 1] = pack_x2<BF16>(e1.x, e1.y);
+          // P in V's type (the MMA wants one type); l sums the unrounded values
+          pk[c] = pack_x2<PV_BF16>(e0.x, e0.y);
+          pk[c + 1] = pack_x2<PV_BF16>(e1.x, e1.y);
+          if constexpr (KIND == kBf16Split) {
+            lo[c] = pack_x2<true>(e0.x - __uint_as_float(pk[c] << 16), e0.y - __uint_as_float(pk[c] & 0xFFFF0000u));
+            lo[c + 1] = pack_x2<true>(e1.x - __uint_as_float(pk[c + 1] << 16),
+                                      e1.y - __uint_as_float(pk[c + 1] & 0xFFFF0000u));
+          }
         }
         tmem_st32(ts + half * 32, pk);
+        if constexpr (KIND == kBf16Split) tmem_st32(ts + 64 + half * 32, lo);
       }
       l_run += (acc0.x + acc0.y) + (acc1.x + acc1.y);
       tc_fence_before();
@@ -452,7 +525,9 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (ok && n_kv > 0) ok = warp_wait(&bar->o_final[t], 0, ctl);
     __syncwarp();
     tc_fence_after();
-    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+    float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+    if constexpr (KIND == kBf16WideV)                   // undo V's power of two
+      inv *= pow2(v_exponent(__ldg(p.v_amax + static_cast<size_t>(b) * p.H_kv + kvh)));
     const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
     const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
     const size_t rg = (static_cast<size_t>(b) * p.H + head) * p.S_q + s_q;
@@ -627,20 +702,33 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p) {
   for (int e = 0; e < E / 2; ++e) dst[e] = pack_x2<true>(out[2 * e], out[2 * e + 1]);
 }
 
-template <int D, bool BF16>
+template <int D, int KIND>
 cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   using C = Cfg<D>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
-  auto kern = diff_attn_kernel<D, BF16>;
+  auto kern = diff_attn_kernel<D, KIND>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
+  if (KIND == kBf16WideV && p.S_kv > 0) {
+    const dim3 grid(static_cast<unsigned>((p.S_kv + kConvRows - 1) / kConvRows), static_cast<unsigned>(p.B * p.H_kv));
+    if ((e = cudaMemsetAsync(p.v_amax, 0, static_cast<size_t>(p.B) * p.H_kv * 4, st)) != cudaSuccess) return e;
+    widen_v_kernel<D, false><<<grid, 256, 0, st>>>(p);
+    widen_v_kernel<D, true><<<grid, 256, 0, st>>>(p);
+  }
   const long long items = static_cast<long long>(p.B) * p.n_groups * p.splits * p.n_rt;
   kern<<<static_cast<unsigned>(items), kThreads, C::SMEM, st>>>(tq, tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
   const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
   diff_merge_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(p);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const DiffParams& p, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, cudaStream_t st) {
+  if (!in_bf16) return launch_t<D, kF16>(p, tq, tk, tv, st);
+  return p.v16 != nullptr ? launch_t<D, kBf16WideV>(p, tq, tk, tv, st) : launch_t<D, kBf16Split>(p, tq, tk, tv, st);
 }
 
 }  // namespace
@@ -655,10 +743,13 @@ int diff_splits(long long items, int S_kv) {
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
+// Whether bf16 operands get an fp16 copy of V: worth its three passes over V
+// once several row tiles walk each V tile.
+bool diff_widens_v(int n_rt) { return n_rt >= 4; }
+
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st) {
-  if (d == 128) return in_bf16 ? launch_t<128, true>(p, tq, tk, tv, st) : launch_t<128, false>(p, tq, tk, tv, st);
-  return in_bf16 ? launch_t<64, true>(p, tq, tk, tv, st) : launch_t<64, false>(p, tq, tk, tv, st);
+  return d == 128 ? launch_d<128>(p, in_bf16, tq, tk, tv, st) : launch_d<64>(p, in_bf16, tq, tk, tv, st);
 }
 
 }  // namespace jattn

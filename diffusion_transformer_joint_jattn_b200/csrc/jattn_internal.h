@@ -163,7 +163,7 @@ struct RotaryParams {
   float scale;                  // factor of the rotated channels
   int inverse;
   long long tokens;             // B * S
-  int units, per, shares;       // set by the launcher
+  int units, tile, groups, shares;   // set by the launcher
 };
 cudaError_t launch_rotary(const RotaryParams& p, int dtype, bool half, cudaStream_t st);
 
@@ -213,10 +213,15 @@ struct DiffParams {
   float* lse;                   // [2][B][H][S_q] or null
   float* part_o;                // [splits][2][B*H*S_q][d]
   float* part_l;                // [splits][2][B*H*S_q], log2 units
+  const __nv_bfloat16* v;       // with v16: the bf16 values it is made from, and their strides in elements
+  int64_t v_stride[3];          //   over (batch entry, head, token)
+  __half* v16;                  // null, or [B][H_kv][S_kv][d]: fp16 copy of v, divided by a power of two per head
+  uint32_t* v_amax;             // with v16: [B][H_kv] bits of the largest finite magnitudes
   uint32_t* status;
   uint64_t timeout_ns;
 };
 int diff_splits(long long items, int S_kv);
+bool diff_widens_v(int n_rt);
 // The maps describe (d, rows, heads or ranges, batch) with boxes of 64 x 128.
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st);

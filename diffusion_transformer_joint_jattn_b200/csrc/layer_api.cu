@@ -76,10 +76,27 @@ jattn_status diff_ranges(const jattn_diff_shape* s, DiffRanges* r) {
   return JATTN_OK;
 }
 
-size_t diff_workspace(const jattn_diff_shape* s, const DiffRanges& r) {
-  if (r.splits == 1) return 0;
-  const size_t rows = static_cast<size_t>(s->B) * s->H * s->S_q;
-  return static_cast<size_t>(r.splits) * 2 * rows * (s->d + 1) * 4;
+// Workspace segments, each 256-byte aligned: the splits' partial results, the
+// fp16 copy of V and its per-head magnitudes.
+struct DiffLayout {
+  size_t part_o, part_l, v16, v_amax, total;
+};
+
+DiffLayout diff_layout(const jattn_diff_shape* s, const DiffRanges& r, bool in_bf16) {
+  DiffLayout L{};
+  size_t off = 0;
+  auto seg = [&](size_t bytes) { const size_t at = off; off += (bytes + 255) / 256 * 256; return at; };
+  if (r.splits > 1) {
+    const size_t rows = static_cast<size_t>(s->B) * s->H * s->S_q;
+    L.part_o = seg(r.splits * 2 * rows * s->d * 4);
+    L.part_l = seg(r.splits * 2 * rows * 4);
+  }
+  if (in_bf16 && jattn::diff_widens_v(r.n_rt) && s->S_kv > 0) {
+    L.v16 = seg(static_cast<size_t>(s->B) * s->H_kv * s->S_kv * s->d * 2);
+    L.v_amax = seg(static_cast<size_t>(s->B) * s->H_kv * 4);
+  }
+  L.total = off;
+  return L;
 }
 
 }  // namespace
@@ -104,11 +121,12 @@ jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors,
                           int32_t S, int32_t d, int32_t parts, int32_t rot, const int32_t* pos,
                           int64_t pos_stride_b, const int32_t* split, const double* freqs,
                           jattn_rotary_layout layout, float scale, int32_t inverse, void* stream) {
-  if (tensors == nullptr || n_tensors < 1 || n_tensors > 2 || B < 0 || S < 0 || d < 2 || parts < 1)
+  if (tensors == nullptr || n_tensors < 1 || n_tensors > 2 || B < 0 || S < 0 || d < 2 || d > 8192 || parts < 1)
     return JATTN_ERR_INVALID_ARG;
   if (!is_float(dtype)) return JATTN_ERR_UNSUPPORTED;
   if (layout != JATTN_ROTARY_INTERLEAVED && layout != JATTN_ROTARY_HALF) return JATTN_ERR_INVALID_ARG;
-  if (d % parts != 0 || d / parts % 2 != 0 || rot < 2 || rot % 2 != 0 || rot > d / parts) return JATTN_ERR_INVALID_ARG;
+  if (d % parts != 0 || d / parts % 2 != 0 || rot < 2 || rot % 2 != 0 || rot > d / parts || d / parts > 512)
+    return JATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return JATTN_ERR_INVALID_ARG;
   jattn::RotaryParams p{};
   p.axis_end[0] = p.axis_end[1] = p.axis_end[2] = rot / 2;
@@ -205,9 +223,10 @@ jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void
   return from_cuda(jattn::launch_linear(p, plan, tma, tx, tw, static_cast<cudaStream_t>(stream)));
 }
 
-size_t jattn_fwd_diff_workspace(const jattn_diff_shape* shape) {
+size_t jattn_fwd_diff_workspace(const jattn_diff_shape* shape, jattn_dtype in_dtype) {
   DiffRanges r;
-  return diff_ranges(shape, &r) == JATTN_OK ? diff_workspace(shape, r) : 0;
+  if (!is_16bit(in_dtype) || diff_ranges(shape, &r) != JATTN_OK) return 0;
+  return diff_layout(shape, r, in_dtype == JATTN_BF16).total;
 }
 
 jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, const void* q, const void* k, const void* v,
@@ -226,7 +245,9 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(lam, 16) ||
       !aligned(norm_w, 16) || !aligned(kv_len, 4) || !aligned(lse, 4))
     return JATTN_ERR_ALIGNMENT;
-  const size_t need = diff_workspace(s, r);
+  const bool in_bf16 = in_dtype == JATTN_BF16;
+  const DiffLayout L = diff_layout(s, r, in_bf16);
+  const size_t need = L.total;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return JATTN_ERR_INVALID_ARG;
   if (need > 0 && !aligned(workspace, 256)) return JATTN_ERR_ALIGNMENT;
   const int64_t items = static_cast<int64_t>(s->B) * r.n_groups * r.n_rt * r.splits;
@@ -252,10 +273,17 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   p.key_mask = key_mask;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (r.splits > 1) {
-    const size_t rows = static_cast<size_t>(s->B) * s->H * s->S_q;
-    p.part_o = static_cast<float*>(workspace);
-    p.part_l = p.part_o + static_cast<size_t>(r.splits) * 2 * rows * s->d;
+    p.part_o = reinterpret_cast<float*>(ws + L.part_o);
+    p.part_l = reinterpret_cast<float*>(ws + L.part_l);
+  }
+  const bool widen = in_bf16 && jattn::diff_widens_v(r.n_rt) && s->S_kv > 0;
+  if (widen) {
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    for (int i = 0; i < 3; ++i) p.v_stride[i] = s->v_stride[i];
+    p.v16 = reinterpret_cast<__half*>(ws + L.v16);
+    p.v_amax = reinterpret_cast<uint32_t*>(ws + L.v_amax);
   }
   p.timeout_ns = kTimeoutNs;
   p.status = jattn::device_status_ptr();
@@ -265,11 +293,14 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   const void* kb = s->S_kv > 0 ? k : q;
   const void* vb = s->S_kv > 0 ? v : q;
   const int64_t skv = s->S_kv > 0 ? s->S_kv : 1;
+  const int64_t D = s->d, contiguous[3] = {s->H_kv * skv * D, skv * D, D};
+  const int64_t* vs = widen ? contiguous : s->v_stride;
+  if (widen) vb = p.v16;
   if (!heads_map(&tq, q, s->d, r.R, r.n_groups, s->B, r.row_stride, r.group_stride, s->q_stride[0]) ||
       !heads_map(&tk, kb, s->d, skv, s->H_kv, s->B, s->k_stride[2], s->k_stride[1], s->k_stride[0]) ||
-      !heads_map(&tv, vb, s->d, skv, s->H_kv, s->B, s->v_stride[2], s->v_stride[1], s->v_stride[0]))
+      !heads_map(&tv, vb, s->d, skv, s->H_kv, s->B, vs[2], vs[1], vs[0]))
     return JATTN_ERR_CUDA;
-  return from_cuda(jattn::launch_diff_attn(p, s->d, in_dtype == JATTN_BF16, tq, tk, tv,
+  return from_cuda(jattn::launch_diff_attn(p, s->d, in_bf16, tq, tk, tv,
                                            static_cast<cudaStream_t>(stream)));
 }
 

@@ -65,14 +65,29 @@ __device__ __forceinline__ void store_from_f32(void* p, int64_t i, int dt, float
 // approximate ones (2^-21 relative or better, far under the 16-bit output's
 // rounding and at the level of the fp32 sum's own).
 __device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float activate(float x, int act) {
+template <int ACT>
+__device__ __forceinline__ float activate_as(float x) {
+  if constexpr (ACT == JATTN_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
+  // 0.5 (1 + tanh u) = sigmoid(2 u)
+  if constexpr (ACT == JATTN_ACT_GELU_TANH) return x * sigmoid_f32(1.5957691216057308f * (x + 0.044715f * x * x * x));
+  if constexpr (ACT == JATTN_ACT_SILU) return x * sigmoid_f32(x);
+  if constexpr (ACT == JATTN_ACT_RELU) return x < 0.f ? 0.f : x;     // keeps NaN
+  return x;
+}
+template <int ACT, int W>
+__device__ __forceinline__ void activate_all(float (&v)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = activate_as<ACT>(v[i]);
+}
+// One branch per array, not per element: the elements' chains interleave.
+template <int W>
+__device__ __forceinline__ void activate(float (&v)[W], int act) {
   switch (act) {
-    case JATTN_ACT_GELU: return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
-    // 0.5 (1 + tanh u) = sigmoid(2 u)
-    case JATTN_ACT_GELU_TANH: return x * sigmoid_f32(1.5957691216057308f * (x + 0.044715f * x * x * x));
-    case JATTN_ACT_SILU: return x * sigmoid_f32(x);
-    case JATTN_ACT_RELU: return x < 0.f ? 0.f : x;     // keeps NaN
-    default: return x;
+    case JATTN_ACT_GELU: activate_all<JATTN_ACT_GELU>(v); break;
+    case JATTN_ACT_GELU_TANH: activate_all<JATTN_ACT_GELU_TANH>(v); break;
+    case JATTN_ACT_SILU: activate_all<JATTN_ACT_SILU>(v); break;
+    case JATTN_ACT_RELU: activate_all<JATTN_ACT_RELU>(v); break;
+    default: break;
   }
 }
 
@@ -121,7 +136,14 @@ __device__ __forceinline__ void store_row(uint32_t* dst, const uint32_t (&w)[WOR
 // shared memory (zeros past N or without a bias).
 __device__ __forceinline__ void finish_row(const LinearParams& p, float (&v)[32], const float* bias, int64_t m, int n) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = activate(v[i] + bias[i], p.act);
+  for (int i = 0; i < 32; i += 4) {
+    const float4 b = *reinterpret_cast<const float4*>(bias + i);
+    v[i] += b.x;
+    v[i + 1] += b.y;
+    v[i + 2] += b.z;
+    v[i + 3] += b.w;
+  }
+  activate(v, p.act);
   const bool f32 = p.out_dtype == JATTN_FP32, bf16 = p.out_dtype == JATTN_BF16;
   const bool whole = n + 32 <= p.N;
   if (p.residual != nullptr) {
@@ -263,26 +285,35 @@ struct TileCfg {
 };
 
 // Stage rows [row0, row0 + rows) x [k0, k0 + 64) of a [n_rows][K] matrix in
-// the 128-byte swizzled layout, zeros outside; lane = two neighbouring k.
+// the 128-byte swizzled layout, zeros outside; lane = two neighbouring k, a
+// warp's loads of 16 rows in flight before the first is stored.
 __device__ __forceinline__ void stage_plain(const uint16_t* g, int64_t ld, int64_t row0, int rows, int64_t n_rows, int k0,
                                             int K, uint8_t* dst) {
+  constexpr int RB = 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k = k0 + 2 * lane;
-#pragma unroll 8
-  for (int r = warp; r < rows; r += 4) {
-    uint32_t lo = 0, hi = 0;
-    if (row0 + r < n_rows) {
-      const uint16_t* src = g + (row0 + r) * ld + k;
-      if (k < K) lo = __ldg(src);
-      if (k + 1 < K) hi = __ldg(src + 1);
+  const bool in0 = k < K, in1 = k + 1 < K;
+  for (int r0 = warp; r0 < rows; r0 += 4 * RB) {
+    uint16_t lo[RB], hi[RB];
+    const uint16_t* src = g + (row0 + r0) * ld + k;
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const bool row_in = r0 + 4 * i < rows && row0 + r0 + 4 * i < n_rows;
+      lo[i] = row_in && in0 ? __ldg(src + 4 * i * ld) : 0;
+      hi[i] = row_in && in1 ? __ldg(src + 4 * i * ld + 1) : 0;
     }
-    const uint32_t off = r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2);
-    *reinterpret_cast<uint32_t*>(dst + off) = lo | (hi << 16);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int r = r0 + 4 * i;
+      if (r < rows)
+        *reinterpret_cast<uint32_t*>(dst + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2)) =
+            static_cast<uint32_t>(lo[i]) | (static_cast<uint32_t>(hi[i]) << 16);
+    }
   }
 }
 
 template <int BN, bool SWAP, bool TMA>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const LinearParams p) {
   using C = TileCfg<BN, SWAP, TMA>;
@@ -409,29 +440,47 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     if (SWAP) {
       const int64_t n = static_cast<int64_t>(ta) * 128 + row;
       const float bias = p.bias != nullptr && n < p.N ? load_as_f32(p.bias, n, p.bias_dtype) : 0.f;
-      auto put = [&](int c, float v) {
+      // columns [c, c + W) of the tile for output channel n
+      auto put = [&](int c, auto& v, int count) {
+        constexpr int W = sizeof(v) / sizeof(float);
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[i] += bias;
+        activate(v, p.act);
         const int64_t m = static_cast<int64_t>(tb) * BN + c;
-        if (m < p.M && n < p.N) {
-          v = activate(v + bias, p.act);
-          if (p.residual != nullptr) v += load_as_f32(p.residual, m * p.ldr + n, p.out_dtype);
-          store_from_f32(p.y, m * p.ldy + n, p.out_dtype, v);
+        if (n >= p.N) return;
+        if (p.residual != nullptr) {
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            if (i < count && m + i < p.M) v[i] += load_as_f32(p.residual, (m + i) * p.ldr + n, p.out_dtype);
         }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          if (i < count && m + i < p.M) store_from_f32(p.y, (m + i) * p.ldy + n, p.out_dtype, v[i]);
       };
       if (split > 1) {
-        for (int c = c_lo; c < c_hi; ++c) {
-          float v = 0.f;
-          for (int q = 0; q < split; ++q) v += ld_cluster(map_rank(red_addr + (c * 128 + row) * 4, q));
-          put(c, v);
-        }
-      } else {
+        constexpr int W = BN / 2;                        // the widest share of a split tile
+        const int count = c_hi - c_lo;
+        float v[W];
 #pragma unroll
+        for (int i = 0; i < W; ++i) v[i] = 0.f;
+        for (int q = 0; q < split; ++q) {
+          const uint32_t at = map_rank(red_addr + (c_lo * 128 + row) * 4, q);
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            if (i < count) v[i] += ld_cluster(at + i * 512);
+        }
+        put(c_lo, v, count);
+      } else {
+#pragma unroll 1
         for (int c = 0; c < BN; c += CH) {
           uint32_t r[32];
           __syncwarp();
           if constexpr (CH == 16) tmem_ld16(tl + c, r);
           else tmem_ld32(tl + c, r);
+          float v[CH];
 #pragma unroll
-          for (int i = 0; i < CH; ++i) put(c + i, __uint_as_float(r[i]));
+          for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[i]);
+          put(c, v, CH);
         }
       }
     } else if constexpr (BN >= 32) {
@@ -454,12 +503,15 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
               finish_row(p, v, sBias + c, m, tb * BN + c);
             } else {
 #pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < w) v[i] += sBias[c + i];
+              activate(v, p.act);
+#pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const int n = tb * BN + c + i;
                 if (i < w && n < p.N) {
-                  float t = activate(v[i] + sBias[c + i], p.act);
-                  if (p.residual != nullptr) t += load_as_f32(p.residual, m * p.ldr + n, p.out_dtype);
-                  store_from_f32(p.y, m * p.ldy + n, p.out_dtype, t);
+                  if (p.residual != nullptr) v[i] += load_as_f32(p.residual, m * p.ldr + n, p.out_dtype);
+                  store_from_f32(p.y, m * p.ldy + n, p.out_dtype, v[i]);
                 }
               }
             }

@@ -8,11 +8,10 @@
 //   gradient: the transpose of a rotation); j = i + 1 or i + rot / 2.
 //
 // Bound by HBM: every element is read and written once and costs a few
-// flops.  A thread owns U channel pairs of one token and walks a share of
-// the heads of q and k with their cosines and sines in registers, so the
-// fp64 angles and the sincos are paid once per share and no table passes
-// through memory.  Its two 16-byte loads of a head are adjacent (interleaved)
-// or rot / 2 apart (half); four heads are in flight per thread.
+// flops.  A block forms the fp64 angles of its tokens once; a thread owns U
+// channel pairs of one token and walks heads of q and k with their cosines and
+// sines in registers.  Its two 16-byte loads of a head are adjacent
+// (interleaved) or rot / 2 apart (half), kHeadsInFlight heads at a time.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -27,7 +26,7 @@ namespace jattn {
 namespace {
 
 constexpr int kRotThreads = 256;
-constexpr int kHeadsInFlight = 4;
+constexpr int kHeadsInFlight = 2;
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -42,70 +41,80 @@ struct alignas(sizeof(T) * U) Vec {
   T e[U];
 };
 
-// One thread: token = (b, s), unit u of a part, heads [share * per, +per) of
-// the H_q * parts + H_k * parts head parts.
+// A block: p.tile tokens x p.units units x p.groups head groups = its 256
+// threads (the last ones may be idle), units fastest, then tokens.  blockIdx.y
+// = share of the heads.  Each (token, pair) angle is formed once per block, in
+// shared memory; a thread then keeps its unit's in registers for all its
+// heads.
 template <typename T, int U, bool HALF>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams p) {
-  const long long gid = static_cast<long long>(blockIdx.x) * kRotThreads + threadIdx.x;
-  const int u = static_cast<int>(gid % p.units);
-  const long long rest = gid / p.units;
-  const long long tok = rest % p.tokens;
-  const long long share = rest / p.tokens;
-  if (share >= p.shares) return;
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const RotaryParams p) {
+  extern __shared__ float2 table[];                    // [tile][rot / 2]
+  const int n_pairs = p.rot / 2;
+  const long long tok0 = static_cast<long long>(blockIdx.x) * p.tile;
+  for (int i = threadIdx.x; i < p.tile * n_pairs; i += kRotThreads) {
+    const long long tok = tok0 + i / n_pairs;
+    const int pair = i % n_pairs;
+    if (tok < p.tokens) {
+      const long long b = tok / p.S, s = tok % p.S;
+      const int axis = pair < p.axis_end[0] ? 0 : (pair < p.axis_end[1] ? 1 : 2);
+      float c, sn;
+      angle_cos_sin(p.pos[b * p.pos_stride_b + s * p.n_axes + axis], p.freqs[pair], c, sn);
+      table[i] = make_float2(c * p.scale, sn * (p.inverse ? -p.scale : p.scale));
+    }
+  }
+  __syncthreads();
+  const int u = threadIdx.x % p.units;
+  const int at = threadIdx.x / p.units;
+  const int tl = at % p.tile, group = at / p.tile;
+  const long long tok = tok0 + tl;
+  if (group >= p.groups || tok >= p.tokens) return;
   const int b = static_cast<int>(tok / p.S), s = static_cast<int>(tok % p.S);
   // channel offsets of the unit's two vectors and its first pair
-  const int n_rot_units = HALF ? p.rot / 2 / U : p.units;
+  const int n_rot_units = HALF ? n_pairs / U : p.units;
   int c0, c1, pair0;
   if (HALF && u < n_rot_units) {
     c0 = u * U;
-    c1 = c0 + p.rot / 2;
+    c1 = c0 + n_pairs;
     pair0 = c0;
   } else if (HALF) {
     c0 = p.rot + (u - n_rot_units) * 2 * U;
     c1 = c0 + U;
-    pair0 = p.rot / 2;                              // past the last pair: copied
+    pair0 = n_pairs;                                   // past the last pair: copied
   } else {
     c0 = u * 2 * U;
     c1 = c0 + U;
     pair0 = u * U;
   }
   float cs[U], sn[U];
-  const int32_t* pos = p.pos + static_cast<long long>(b) * p.pos_stride_b + static_cast<long long>(s) * p.n_axes;
 #pragma unroll
   for (int i = 0; i < U; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-    const int pair = pair0 + i;
-    if (pair < p.rot / 2) {
-      const int axis = pair < p.axis_end[0] ? 0 : (pair < p.axis_end[1] ? 1 : 2);
-      angle_cos_sin(pos[axis], p.freqs[pair], cs[i], sn[i]);
-      cs[i] *= p.scale;
-      sn[i] *= p.inverse ? -p.scale : p.scale;
-    }
+    const float2 e = pair0 + i < n_pairs ? table[tl * n_pairs + pair0 + i] : make_float2(1.f, 0.f);
+    cs[i] = e.x;
+    sn[i] = e.y;
   }
   const int n = p.d / p.parts;
   const int total = (p.H[0] + p.H[1]) * p.parts;
-  const int lo = static_cast<int>(share) * p.per, hi = min(lo + p.per, total);
+  const int step = p.groups * p.shares;                // head parts first, first + step, ...
   using V = Vec<T, U>;
-  for (int h0 = lo; h0 < hi; h0 += kHeadsInFlight) {
+  for (int h0 = blockIdx.y * p.groups + group; h0 < total; h0 += step * kHeadsInFlight) {
     V a[kHeadsInFlight], c[kHeadsInFlight];
     T* dst[kHeadsInFlight];
 #pragma unroll
     for (int k = 0; k < kHeadsInFlight; ++k) {
-      const int hp = min(h0 + k, hi - 1);
+      const int hp = min(h0 + k * step, total - 1);
       const int head = hp / p.parts, part = hp % p.parts;
       const int t = head < p.H[0] ? 0 : 1;
       const int h = t == 0 ? head : head - p.H[0];
       const T* src = static_cast<const T*>(p.x[t]) + b * p.xs[t][0] + s * p.xs[t][1] + h * p.xs[t][2] + part * n;
       dst[k] = static_cast<T*>(p.y[t]) + b * p.ys[t][0] + s * p.ys[t][1] + h * p.ys[t][2] + part * n;
-      if (h0 + k < hi) {
+      if (h0 + k * step < total) {
         a[k] = *reinterpret_cast<const V*>(src + c0);
         c[k] = *reinterpret_cast<const V*>(src + c1);
       }
     }
 #pragma unroll
     for (int k = 0; k < kHeadsInFlight; ++k) {
-      if (h0 + k >= hi) break;
+      if (h0 + k * step >= total) break;
       // pairs past rot have cos 1 and sin 0, but are copied: 0 * inf is NaN
       if (HALF) {
         if (u < n_rot_units) {
@@ -126,7 +135,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          if (pair0 + i < p.rot / 2) {
+          if (pair0 + i < n_pairs) {
             float y0, y1;
             rotate_pair(to_f32(v[2 * i]), to_f32(v[2 * i + 1]), cs[i], sn[i], y0, y1);
             v[2 * i] = from_f32<T>(y0);
@@ -166,19 +175,27 @@ template <typename T, int U>
 cudaError_t launch_u(RotaryParams p, bool half, cudaStream_t st) {
   const int total = (p.H[0] + p.H[1]) * p.parts;
   p.units = p.d / p.parts / (2 * U);
-  // Heads per thread: as many as leave two full waves of threads (148 SMs x
-  // 2048) busy, at least one batch of kHeadsInFlight (fewer heads per thread
-  // only repeat the angles once the GPU is full).
-  const long long owners = p.tokens * p.units;
-  long long shares = (2ll * 148 * 2048 + owners - 1) / owners;
-  const long long most = (total + kHeadsInFlight - 1) / kHeadsInFlight;
-  if (shares > most) shares = most;
-  p.per = static_cast<int>((total + shares - 1) / shares);
-  p.shares = (total + p.per - 1) / p.per;
-  const long long blocks = (owners * p.shares + kRotThreads - 1) / kRotThreads;
+  if (p.units > kRotThreads) return cudaErrorInvalidConfiguration;
+  // Tokens per block: 8 heads of each in flight side by side where there are
+  // that many tokens for every SM; then as many head groups as threads are left.
+  const int slots = kRotThreads / p.units;
+  p.tile = slots / 8 > 0 ? slots / 8 : 1;
+  while (p.tile > 1 && p.tokens / p.tile < 2 * 148) p.tile /= 2;
+  while (p.tile > 1 && p.tile * p.rot * 4 > 32768) p.tile /= 2;
+  p.groups = slots / p.tile;
+  if (p.groups > total) p.groups = total;
+  const long long blocks = (p.tokens + p.tile - 1) / p.tile;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
-  if (half) rotary_kernel<T, U, true><<<static_cast<unsigned>(blocks), kRotThreads, 0, st>>>(p);
-  else rotary_kernel<T, U, false><<<static_cast<unsigned>(blocks), kRotThreads, 0, st>>>(p);
+  // few tokens: the heads over more blocks
+  const int most = (total + p.groups - 1) / p.groups;
+  long long shares = (2 * 148 + blocks - 1) / blocks;
+  if (shares > most) shares = most;
+  p.shares = static_cast<int>(shares);
+  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(p.shares));
+  const size_t smem = static_cast<size_t>(p.tile) * (p.rot / 2) * sizeof(float2);
+  if (smem > 49152) return cudaErrorInvalidConfiguration;
+  if (half) rotary_kernel<T, U, true><<<grid, kRotThreads, smem, st>>>(p);
+  else rotary_kernel<T, U, false><<<grid, kRotThreads, smem, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -23,6 +23,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -54,22 +55,11 @@ class Shape(ctypes.Structure):
                 ("S_img", ctypes.c_int32), ("S_ref", ctypes.c_int32), ("d", ctypes.c_int32)]
 
 
-class RotaryTensor(ctypes.Structure):
-    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("H", ctypes.c_int32),
-                ("x_stride", ctypes.c_int64 * 3), ("y_stride", ctypes.c_int64 * 3)]
-
-
-class LinearShape(ctypes.Structure):
-    _fields_ = [("M", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("ldx", ctypes.c_int64),
-                ("ldw", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldr", ctypes.c_int64),
-                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("bias_dtype", ctypes.c_int32),
-                ("act", ctypes.c_int32)]
-
-
-class DiffShape(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("S_q", ctypes.c_int32),
-                ("S_kv", ctypes.c_int32), ("d", ctypes.c_int32), ("q_stride", ctypes.c_int64 * 3),
-                ("k_stride", ctypes.c_int64 * 3), ("v_stride", ctypes.c_int64 * 3)]
+# jattn_rotary_tensor, jattn_linear_shape and jattn_diff_shape, packed: a
+# ctypes.Structure costs several times as much per call.
+_ROTARY_TENSOR = struct.Struct("@PPi0q6q")
+_LINEAR_SHAPE = struct.Struct("@3i0q4q4i")
+_DIFF_SHAPE = struct.Struct("@6i0q9q")
 
 
 class JattnError(RuntimeError):
@@ -112,12 +102,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jattn_fwd_block_sparse.argtypes = [sp, i32, vp, vp, vp, f32, vp, ctypes.c_size_t, vp, vp, vp, vp, f32, vp]
     lib.jattn_fwd_block_sparse_workspace.argtypes = [sp]
     lib.jattn_fwd_fp8.argtypes = [sp, vp, vp, vp, vp, vp, vp, f32, vp]
-    lib.jattn_rotary.argtypes = [ctypes.POINTER(RotaryTensor), i32, i32, i32, i32, i32, i32, i32, vp, ctypes.c_int64,
+    lib.jattn_rotary.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, vp, ctypes.c_int64,
                                  ctypes.POINTER(i32), vp, i32, f32, i32, vp]
-    lib.jattn_linear.argtypes = [ctypes.POINTER(LinearShape), vp, vp, vp, vp, vp, vp]
-    lib.jattn_fwd_diff.argtypes = [ctypes.POINTER(DiffShape), i32, vp, vp, vp, vp, f32, vp, f32, vp, vp, vp,
+    lib.jattn_linear.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+    lib.jattn_fwd_diff.argtypes = [vp, i32, vp, vp, vp, vp, f32, vp, f32, vp, vp, vp,
                                    ctypes.c_size_t, vp, vp, f32, vp]
-    lib.jattn_fwd_diff_workspace.argtypes = [ctypes.POINTER(DiffShape)]
+    lib.jattn_fwd_diff_workspace.argtypes = [vp, i32]
     lib.jattn_device_status.argtypes = [vp, i32, ctypes.POINTER(ctypes.c_uint32)]
     lib.jattn_last_device_status.argtypes = [vp]
     lib.jattn_selftest_wait_timeout.argtypes = [i32, vp]
@@ -628,7 +618,6 @@ def joint_attention(qkv_txt, qkv_img, qkv_ref, pos, split, theta: float = 10000.
 _FLOAT_CODE = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
 _ACT_CODE = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
 _ROTARY_LAYOUT = {"interleaved": 0, "half": 1}
-_I64x3 = ctypes.c_int64 * 3
 
 
 def _enqueue(dev, stream, inputs, call):
@@ -636,8 +625,8 @@ def _enqueue(dev, stream, inputs, call):
     device's current one when None).  On a stream that is not the current one
     the outputs are allocated for that stream, and the inputs are kept from
     reuse until its work is done."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        return call(torch.cuda.current_stream().cuda_stream)
+    if stream is None and dev.index == torch._C._cuda_getDevice():
+        return call(torch._C._cuda_getCurrentRawStream(dev.index))
     with torch.cuda.device(dev):
         if stream is None or stream == torch.cuda.current_stream():
             return call(torch.cuda.current_stream().cuda_stream)
@@ -708,12 +697,6 @@ def rotary_freqs(dim=None, theta: float = 10000.0, scaling: str = "none", factor
     return torch.cat(freqs).to("cuda" if device is None else device), scale
 
 
-def _rotary_tensor(x, y):
-    xs, ys = x.stride(), y.stride()
-    return RotaryTensor(x.data_ptr(), y.data_ptr(), x.shape[2], _I64x3(xs[0], xs[1], xs[2]),
-                        _I64x3(ys[0], ys[1], ys[2]))
-
-
 def rotary(q, k, pos, freqs, split: Optional[Sequence[int]] = None, layout: str = "interleaved", parts: int = 1,
            scale: float = 1.0, inverse: bool = False, out=None, stream=None):
     """Rotary embedding of q [B, S, H, d] and k [B, S, H_k, d] (or None) in one
@@ -771,7 +754,8 @@ def rotary(q, k, pos, freqs, split: Optional[Sequence[int]] = None, layout: str 
 
     def call(st):
         ys = tuple(torch.empty(x.shape, dtype=dtype, device=dev) for x in xs) if out is None else out
-        ts = (RotaryTensor * len(xs))(*[_rotary_tensor(x, y) for x, y in zip(xs, ys)])
+        ts = b"".join([_ROTARY_TENSOR.pack(x.data_ptr(), y.data_ptr(), x.shape[2], *x.stride()[:3], *y.stride()[:3])
+                       for x, y in zip(xs, ys)])
         _check(lib.jattn_rotary(ts, len(xs), _FLOAT_CODE[dtype], B, S, d, parts, 2 * freqs.numel(), pos.data_ptr(),
                                 per_batch, sp, freqs.data_ptr(), _ROTARY_LAYOUT[layout], scale, inverse, st),
                "jattn_rotary")
@@ -826,9 +810,9 @@ def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtyp
 
     def call(st):
         y = torch.empty(shape, dtype=out_dtype, device=dev) if out is None else out
-        sh = LinearShape(M, N, K, ldx, ldw, ldy, ldr, _FLOAT_CODE[x.dtype], _FLOAT_CODE[out_dtype],
-                         0 if bias is None else _FLOAT_CODE[bias.dtype], _ACT_CODE[act])
-        _check(lib.jattn_linear(ctypes.byref(sh), x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
+        sh = _LINEAR_SHAPE.pack(M, N, K, ldx, ldw, ldy, ldr, _FLOAT_CODE[x.dtype], _FLOAT_CODE[out_dtype],
+                                0 if bias is None else _FLOAT_CODE[bias.dtype], _ACT_CODE[act])
+        _check(lib.jattn_linear(sh, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
                                 None if residual is None else residual.data_ptr(), y.data_ptr(), st), "jattn_linear")
         return y
     return _enqueue(dev, stream, (x, w, bias, residual, out), call)
@@ -888,8 +872,8 @@ def fwd_diff(q, k, v, lam, lambda_init: float, norm_w=None, eps: float = 1e-5, k
         _on(t, name, dev, dtypes)
         if tuple(t.shape) != n or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {n}, got {tuple(t.shape)}")
-    sh = DiffShape(B, H, H_kv, S_q, S_kv, d, _I64x3(*q.stride()[:3]), _I64x3(*k.stride()[:3]), _I64x3(*v.stride()[:3]))
-    need = lib.jattn_fwd_diff_workspace(ctypes.byref(sh))
+    sh = _DIFF_SHAPE.pack(B, H, H_kv, S_q, S_kv, d, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
+    need = lib.jattn_fwd_diff_workspace(sh, _FLOAT_CODE[q.dtype])
     if workspace is not None:
         _on(workspace, "workspace", dev, (torch.uint8,))
         if not workspace.is_contiguous() or workspace.numel() < need:
@@ -904,7 +888,7 @@ def fwd_diff(q, k, v, lam, lambda_init: float, norm_w=None, eps: float = 1e-5, k
         if ll is None and want_lse:
             ll = torch.empty(2, B, H, S_q, dtype=torch.float32, device=dev)
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        _check(lib.jattn_fwd_diff(ctypes.byref(sh), _FLOAT_CODE[q.dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(),
+        _check(lib.jattn_fwd_diff(sh, _FLOAT_CODE[q.dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                   lam.data_ptr(), lambda_init, ptr(norm_w), eps, ptr(kv_len), ptr(key_mask), ptr(ws),
                                   0 if ws is None else ws.numel(), oo.data_ptr(), ptr(ll), softmax_scale, st),
                "jattn_fwd_diff")

@@ -383,7 +383,8 @@ typedef struct {
  *   t = pos * freqs[pair] formed in fp64, the products in fp32, one rounding.
  * The channels of a head are `parts` equal parts (the two maps of
  * differential attention), each rotated by itself: its first rot channels
- * (even, in [2, d / parts]; d / parts even) turn, the others are copied.
+ * (even, in [2, d / parts]; d / parts even, at most 512) turn, the others are
+ * copied.
  *   tensors   : host array of n_tensors (1 or 2).
  *   dtype     : JATTN_BF16, JATTN_FP16 or JATTN_FP32, input and output.
  *   pos       : int32 [B or 1][S][n_axes], n_axes = split ? 3 : 1;
@@ -471,13 +472,14 @@ typedef struct {
  *   lse      : fp32 [2][B][H][S_q], the natural-log sum-exp of both maps
  *              (-inf for a row without a key), or NULL.
  *   softmax_scale <= 0 selects 1 / sqrt(d / 2).
- *   workspace: device scratch of at least jattn_fwd_diff_workspace(shape)
+ *   workspace: device scratch of at least jattn_fwd_diff_workspace()
  *              bytes, 256-byte aligned (NULL where that is 0).  Calls that
  *              may overlap on the GPU need one each.
  * Pointers 16-byte aligned (kv_len, lse 4; key_mask 1).  Errors as
  * jattn_fwd_bf16.  B or S_q of 0 is no work and JATTN_OK.
  */
-size_t jattn_fwd_diff_workspace(const jattn_diff_shape* shape);   /* 0: none needed, or invalid arguments */
+/* 0: none needed, or invalid arguments */
+size_t jattn_fwd_diff_workspace(const jattn_diff_shape* shape, jattn_dtype in_dtype);
 jattn_status jattn_fwd_diff(const jattn_diff_shape* shape, jattn_dtype in_dtype, const void* q, const void* k,
                             const void* v, const float* lam, float lambda_init, const float* norm_w, float eps,
                             const int32_t* kv_len, const uint8_t* key_mask, void* workspace,
