@@ -20,11 +20,20 @@
 //               through shared memory.
 //   warp 8      MMA issuer, warp 9 TMA producer, warp 10 zeroes the V rows of
 //               masked keys in shared memory (their P is 0, and 0 * NaN would
-//               not be); warp 11 idle.
+//               not be); warp 11 finds the CTA's share of the work.
+// Keys are walked in halves of 64: each map has two S buffers of 64 TMEM
+// columns, and Q.K^T of half i + 2 is issued behind P.V of half i, so S of
+// half i + 1 is there when the softmax of half i ends and the softmax warps
+// do not wait for the tensor pipe.  TMEM: S [0, 256), O_1 [256, +d), O_2 [384,
+// +d).
 // Query rows of the heads that share a K/V head are packed into one row
 // range where the strides allow it, so a cache is read once for the group.
-// Few rows over a long cache: the keys are split over CTAs that write their
-// normalised partial outputs and log-sum-exps, merged by a second kernel.
+// Work: an item is one 128-row tile of one range.  Whole waves of items go
+// one item at a time to the SMs (neighbouring CTAs then walk the same keys);
+// the items of the last, partial wave -- all items of a single-token call --
+// are cut into equal runs of key tiles, one per CTA.  A CTA that has a part of
+// an item writes its normalised output and log-sum-exp; a second kernel
+// merges the parts.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,14 +49,17 @@ namespace {
 
 constexpr int BM = 128;                // query rows per tile
 constexpr int BN = 128;                // keys per tile
-constexpr int kMmaWarp = 8, kProducerWarp = 9, kMaskWarp = 10;
+constexpr int kMmaWarp = 8, kProducerWarp = 9, kMaskWarp = 10, kShareWarp = 11;
 constexpr int kThreads = 384;
-// 2 x 128 x 216 + 128 x 72 = 64512 = 384 x 168, what the block launches with
-constexpr uint32_t kRegsSoftmax = 216, kRegsOther = 72;
+// Register split after setmaxnreg, together the 384 x 168 the block launches
+// with; each leaves the softmax and the single-thread roles without spills
+// (-Xptxas -v).
+template <int D> __host__ __device__ constexpr uint32_t regs_softmax() { return D == 128 ? 208u : 216u; }
+template <int D> __host__ __device__ constexpr uint32_t regs_other() { return (kThreads * 168u - 256u * regs_softmax<D>()) / 128u; }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 15.0f;   // log2 units; P <= 2^15 in 16 bits
 
-__host__ __device__ constexpr uint32_t col_s(int t) { return static_cast<uint32_t>(t) * 128u; }
+__host__ __device__ constexpr uint32_t col_s(int t, int buf) { return static_cast<uint32_t>(t * 128 + buf * 64); }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(t) * 128u; }
 
 template <int D>
@@ -58,40 +70,59 @@ struct Cfg {
   static constexpr int TB = BM * RB;
   static constexpr int KS = D == 128 ? 3 : 4;
   static constexpr int VS = D == 128 ? 3 : 4;
-  static constexpr int SMEM = (1 + KS + VS) * TB + 256 + 1024;
+  static constexpr int EX = 4 * BM * 4;               // row sums and squares of both maps
+  static constexpr int SLACK = 704;                   // to align the tiles to 1024 bytes
+  static constexpr int SMEM = (1 + KS + VS) * TB + EX + 320 + SLACK;
+};
+
+// This CTA's run of the shared items' key tiles: from tile `off` of item
+// `item` on, `count` tiles.
+struct Share {
+  long long item, count;
+  int off;
 };
 
 struct __align__(8) Bars {
-  uint64_t q_full;
+  uint64_t q_full, q_empty;
   uint64_t k_full[4], k_empty[4];
   uint64_t v_full[4], v_empty[4], v_ready[4];
-  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t s_full[2][2], p_full[2][2];                // [map][buffer]
   uint64_t exchange[2];
-  uint64_t mma_final;
+  Share share;
   uint32_t tmem_base;
   uint32_t abort;
 };
-
+// Every lane waits; the warp goes on together, or not at all.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
-  uint64_t t0 = 0;
-  for (uint32_t i = 0;; ++i) {
-    const bool ok = mbar_try_wait(bar, parity);
-    if (__all_sync(0xffffffffu, ok)) return true;
-    if ((i & 63u) == 63u) {
-      int stop = 0;
-      if (lane_id() == 0) {
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        if (*ctl.abort) stop = 1;
-        else if (now - t0 > ctl.limit_ns) {
-          atomicOr(ctl.status, JATTN_DEV_TIMEOUT);
-          *ctl.abort = 1u;
-          stop = 1;
-        }
-      }
-      if (__shfl_sync(0xffffffffu, stop, 0)) return false;
-    }
-  }
+  const bool ok = mbar_wait(bar, parity, ctl);
+  return __all_sync(0xffffffffu, ok);
+}
+// The MMA and commit instructions by the lane with `lead` set.
+__device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+      ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
 }
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
   const uint64_t t0 = globaltimer_ns();
@@ -126,19 +157,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float row_max(const float (&v)[BN]) {
-  float a[43];
+__device__ __forceinline__ float row_max(const float (&v)[64]) {
+  float a[21];
 #pragma unroll
-  for (int i = 0; i < 42; ++i) a[i] = max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
-  a[42] = fmaxf(v[126], v[127]);
-  float c[15];
+  for (int i = 0; i < 21; ++i) a[i] = max3(v[3 * i], v[3 * i + 1], v[3 * i + 2]);
+  float c[7];
 #pragma unroll
-  for (int i = 0; i < 14; ++i) c[i] = max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
-  c[14] = a[42];
-  float e[5];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) e[i] = max3(c[3 * i], c[3 * i + 1], c[3 * i + 2]);
-  return max3(e[0], e[1], fmaxf(e[2], fmaxf(e[3], e[4])));
+  for (int i = 0; i < 7; ++i) c[i] = max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
+  return max3(max3(c[0], c[1], c[2]), max3(c[3], c[4], c[5]), fmaxf(c[6], v[63]));
 }
 
 // Keys of batch entry b (the length clamped into the cache).
@@ -213,6 +239,111 @@ __device__ __forceinline__ float lambda_of(const DiffParams& p, int head, int dm
   return expf(s1) - expf(s2) + p.lambda_init;
 }
 
+// Key tiles of an item of batch entry b; an empty one counts as one tile, so
+// that some CTA writes its zeros.
+__device__ __forceinline__ int tiles_of(const DiffParams& p, int b) { return max((key_count(p, b) + BN - 1) / BN, 1); }
+// Tiles of the shared items (numbers >= p.items_whole) of batch entry b.
+__device__ __forceinline__ long long shared_tiles(const DiffParams& p, int b) {
+  const long long per = static_cast<long long>(p.n_groups) * p.n_rt, lo = b * per;
+  const long long from = max(lo, p.items_whole);
+  return lo + per <= from ? 0 : (lo + per - from) * tiles_of(p, b);
+}
+// A whole warp: the sum of shared_tiles over the first nb batch entries.
+__device__ __forceinline__ long long shared_prefix(const DiffParams& p, int nb) {
+  long long t = 0;
+  for (int b = threadIdx.x & 31; b < nb; b += 32) t += shared_tiles(p, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+// A whole warp: the item that holds tile g of the shared items, and g's place
+// in it.
+__device__ __forceinline__ void locate(const DiffParams& p, long long g, long long& item, int& off) {
+  const int lane = threadIdx.x & 31;
+  int b = 0;
+  for (int b0 = 0;; b0 += 32) {
+    const long long mine = b0 + lane < p.B ? shared_tiles(p, b0 + lane) : 0;
+    long long sum = mine;                               // inclusive, over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += t;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, g < sum);
+    const long long before = sum - mine;
+    if (past != 0) {
+      const int l = __ffs(past) - 1;
+      b = b0 + l;
+      g -= __shfl_sync(0xffffffffu, before, l);
+      break;
+    }
+    g -= __shfl_sync(0xffffffffu, sum, 31);
+    if (b0 + 32 >= p.B) {                               // g past the end: not called so
+      b = p.B - 1;
+      g = 0;
+      break;
+    }
+  }
+  const long long per = static_cast<long long>(p.n_groups) * p.n_rt;
+  const int nt = tiles_of(p, b);
+  item = max(b * per, p.items_whole) + g / nt;
+  off = static_cast<int>(g % nt);
+}
+// First of the `total` shared tiles that CTA c takes.
+__device__ __forceinline__ long long share_start(long long total, int c, int ctas) { return total * c / ctas; }
+
+// One piece of work: key tiles [t0, t0 + n_kv) of an item.
+struct Segment {
+  int b, gi, rt, len, t0, n_kv, n_half;
+  bool whole, from_start;        // all of the item's tiles; starts with its first
+};
+__device__ __forceinline__ Segment segment_of(const DiffParams& p, long long item, int t0, int n, int nt) {
+  Segment s;
+  s.rt = static_cast<int>(item % p.n_rt);
+  const int g = static_cast<int>(item / p.n_rt);
+  s.gi = g % p.n_groups;
+  s.b = g / p.n_groups;
+  s.len = key_count(p, s.b);
+  s.t0 = t0;
+  s.n_kv = s.len > 0 ? n : 0;
+  // a last tile of at most 64 keys is one half
+  s.n_half = 2 * s.n_kv - (s.n_kv > 0 && s.len - (t0 + n - 1) * BN <= 64 ? 1 : 0);
+  s.whole = n == nt;
+  s.from_start = t0 == 0;
+  return s;
+}
+// This CTA's work in order: whole items first, then its share of the others.
+struct Walk {
+  long long item, left;
+  int off;
+  bool whole;
+  __device__ __forceinline__ Walk(const DiffParams& p, const Share& s) {
+    whole = blockIdx.x < p.items_whole;
+    item = whole ? blockIdx.x : s.item;
+    left = s.count;
+    off = whole ? 0 : s.off;
+  }
+  __device__ __forceinline__ bool next(const DiffParams& p, const Share& share, Segment& s) {
+    if (!whole && left <= 0) return false;
+    const int nt = tiles_of(p, static_cast<int>(item / (p.n_groups * p.n_rt)));
+    const int n = whole ? nt : static_cast<int>(min(static_cast<long long>(nt - off), left));
+    s = segment_of(p, item, off, n, nt);
+    if (whole) {
+      item += gridDim.x;
+      if (item >= p.items_whole) {
+        whole = false;
+        item = share.item;
+        off = share.off;
+      }
+    } else {
+      left -= n;
+      off = 0;
+      ++item;
+    }
+    return true;
+  }
+};
+
 // KIND: the operands' types and how P keeps its precision.  P in bf16 alone
 // costs the output 1.9e-3 (relative, N(0, 1) inputs), more than the bf16
 // output's own rounding, because the difference of the maps cancels.
@@ -229,38 +360,25 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   using C = Cfg<D>;
   constexpr int DM = D / 2;
   constexpr bool QK_BF16 = KIND != kF16, PV_BF16 = KIND == kBf16Split;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t* sQ = smem;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t skew = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  if (skew > static_cast<uint32_t>(C::SLACK)) {       // uniform; the layout gives no such base
+    if (threadIdx.x == 0) atomicOr(p.status, JATTN_DEV_CHECK);
+    return;
+  }
+  uint8_t* sQ = smem_raw + skew;
   uint8_t* sK = sQ + C::TB;
   uint8_t* sV = sK + C::KS * C::TB;
-  Bars* bar = reinterpret_cast<Bars*>(sV + C::VS * C::TB);
-  static_assert(sizeof(Bars) <= 256, "room for the barriers");
-  // the epilogue's exchange lies over the Q tile, whose last use o_final proves
-  float* sL = reinterpret_cast<float*>(sQ);                   // [2][BM] 1 / l
+  float* sL = reinterpret_cast<float*>(sV + C::VS * C::TB);   // [2][BM] 1 / l
   float* sSq = sL + 2 * BM;                                   // [2][BM] sums of squares
+  Bars* bar = reinterpret_cast<Bars*>(sSq + 2 * BM);
+  static_assert(sizeof(Bars) <= 320, "room for the barriers");
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // this CTA's item: batch entry, group of heads, split of the keys, row tile
-  int it = blockIdx.x;
-  const int rt = it % p.n_rt;
-  it /= p.n_rt;
-  const int sp = it % p.splits;
-  it /= p.splits;
-  const int gi = it % p.n_groups, b = it / p.n_groups;
-  const int kvh = static_cast<int>(static_cast<long long>(gi) * p.H_kv / p.n_groups);
-  const int len = key_count(p, b);
-  const int n_total = (len + BN - 1) / BN;
-  const int t0 = static_cast<int>(static_cast<long long>(n_total) * sp / p.splits);
-  const int n_kv = static_cast<int>(static_cast<long long>(n_total) * (sp + 1) / p.splits) - t0;
-  const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(b) * p.S_kv : nullptr;
-  // V rows of masked keys have to be zeroed: a mask, or a length inside the
-  // cache (rows past the cache arrive as zeros from TMA; the converted V has
-  // its masked rows zeroed)
-  const bool fix = KIND != kBf16WideV && (mask != nullptr || len < p.S_kv);
-
+  // from one lane, so that the compiler sees the roles' branches as uniform
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bar->q_full, 1);
+    mbar_init(&bar->q_empty, 1);
     for (int s = 0; s < C::KS; ++s) {
       mbar_init(&bar->k_full[s], 1);
       mbar_init(&bar->k_empty[s], 1);
@@ -271,12 +389,12 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       mbar_init(&bar->v_ready[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&bar->s_full[t], 1);
-      mbar_init(&bar->p_full[t], BM);
-      mbar_init(&bar->o_final[t], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar->s_full[t][i], 1);
+        mbar_init(&bar->p_full[t][i], BM / 32);
+      }
       mbar_init(&bar->exchange[t], 2 * BM);
     }
-    mbar_init(&bar->mma_final, 1);
     bar->abort = 0;
     fence_mbarrier_init();
   }
@@ -285,221 +403,313 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tmem_alloc(&bar->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  if (warp == kShareWarp) {
+    Share mine{0, 0, 0};
+    if (p.items > p.items_whole) {
+      const long long total = shared_prefix(p, p.B);
+      const long long g0 = share_start(total, blockIdx.x, gridDim.x), g1 = share_start(total, blockIdx.x + 1, gridDim.x);
+      mine.count = g1 - g0;
+      if (g1 > g0) locate(p, g0, mine.item, mine.off);
+    }
+    if (lane == 0) bar->share = mine;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
+  const Share share = bar->share;
   const WaitCtl ctl{&bar->abort, p.status, p.timeout_ns};
+  auto kv_head = [&](int gi) { return static_cast<int>(static_cast<long long>(gi) * p.H_kv / p.n_groups); };
+  // V rows of masked keys have to be zeroed: a mask, or a length inside the
+  // cache (rows past the cache arrive as zeros from TMA; the converted V has
+  // its masked rows zeroed)
+  auto fixes = [&](const Segment& s) { return KIND != kBf16WideV && (p.key_mask != nullptr || s.len < p.S_kv); };
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(regs_other<D>()));
     if (warp == kProducerWarp) {
-      if (lane == 0 && n_kv > 0) {
-        mbar_arrive_expect_tx(&bar->q_full, C::TB);
-        for (int x = 0; x < C::NBOX; ++x) tma_load_4d(&tmQ, &bar->q_full, sQ + x * C::BOXB, x * 64, rt * BM, gi, b);
-        int nk = 0, nv = 0;
-        for (int j = 0; j < n_kv; ++j) {
-          const int ks = nk % C::KS;
-          if (!mbar_wait(&bar->k_empty[ks], ((nk / C::KS) & 1) ^ 1, ctl)) break;
-          mbar_arrive_expect_tx(&bar->k_full[ks], C::TB);
+      if (lane == 0) {
+        int nq = 0, nk = 0;                             // Q tiles, key tiles (K and V) loaded so far
+        bool v_behind = false;                          // the last key tile's V was not issued
+        Segment s;
+        bool ok = true;
+        for (Walk walk(p, share); ok && walk.next(p, share, s);) {
+          if (s.n_kv == 0) continue;
+          // the Q buffer is free once the previous segment's Q.K^T are done
+          if (nq > 0 && !mbar_wait(&bar->q_empty, (nq - 1) & 1, ctl)) break;
+          mbar_arrive_expect_tx(&bar->q_full, C::TB);
           for (int x = 0; x < C::NBOX; ++x)
-            tma_load_4d(&tmK, &bar->k_full[ks], sK + ks * C::TB + x * C::BOXB, x * 64, (t0 + j) * BN, kvh, b);
-          ++nk;
-          const int vs = nv % C::VS;
-          if (!mbar_wait(&bar->v_empty[vs], ((nv / C::VS) & 1) ^ 1, ctl)) break;
-          mbar_arrive_expect_tx(&bar->v_full[vs], C::TB);
-          for (int x = 0; x < C::NBOX; ++x)
-            tma_load_4d(&tmV, &bar->v_full[vs], sV + vs * C::TB + x * C::BOXB, x * 64, (t0 + j) * BN, kvh, b);
-          ++nv;
+            tma_load_4d(&tmQ, &bar->q_full, sQ + x * C::BOXB, x * 64, s.rt * BM, s.gi, s.b);
+          ++nq;
+          const int kvh = kv_head(s.gi);
+          for (int j = 0; j < s.n_kv; ++j, ++nk) {
+            const int ks = nk % C::KS, vs = nk % C::VS;
+            ok = mbar_wait(&bar->k_empty[ks], ((nk / C::KS) & 1) ^ 1, ctl);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&bar->k_full[ks], C::TB);
+            for (int x = 0; x < C::NBOX; ++x)
+              tma_load_4d(&tmK, &bar->k_full[ks], sK + ks * C::TB + x * C::BOXB, x * 64, (s.t0 + j) * BN, kvh, s.b);
+            ok = mbar_wait(&bar->v_empty[vs], ((nk / C::VS) & 1) ^ 1, ctl);
+            if (!ok) {
+              v_behind = true;
+              ++nk;
+              break;
+            }
+            mbar_arrive_expect_tx(&bar->v_full[vs], C::TB);
+            for (int x = 0; x < C::NBOX; ++x)
+              tma_load_4d(&tmV, &bar->v_full[vs], sV + vs * C::TB + x * C::BOXB, x * 64, (s.t0 + j) * BN, kvh, s.b);
+          }
         }
         // every load issued must have landed before the CTA may exit
-        drain_wait(&bar->q_full, 0, ctl);
-        for (int i = nk > C::KS ? nk - C::KS : 0; i < nk; ++i) drain_wait(&bar->k_full[i % C::KS], (i / C::KS) & 1, ctl);
-        for (int i = nv > C::VS ? nv - C::VS : 0; i < nv; ++i) drain_wait(&bar->v_full[i % C::VS], (i / C::VS) & 1, ctl);
+        if (nq > 0) drain_wait(&bar->q_full, (nq - 1) & 1, ctl);
+        for (int i = max(nk - C::KS, 0); i < nk; ++i) drain_wait(&bar->k_full[i % C::KS], (i / C::KS) & 1, ctl);
+        const int nv = nk - (v_behind ? 1 : 0);
+        for (int i = max(nv - C::VS, 0); i < nv; ++i) drain_wait(&bar->v_full[i % C::VS], (i / C::VS) & 1, ctl);
       }
     } else if (warp == kMmaWarp) {
-      if (lane == 0 && n_kv > 0) {
-        const uint32_t idesc_qk = instr_desc(QK_BF16, QK_BF16, 0, BM, BN);
-        const uint32_t idesc_pv = instr_desc(PV_BF16, PV_BF16, 1, BM, D);
-        const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
-        bool any_mma = false;
-        auto issue_qk = [&](int t, int ks) {
+      // The whole warp walks, one lane issues: the descriptors are then warp
+      // uniform and live in uniform registers.  With one lane walking, each
+      // MMA cost 72 clocks to issue (measured; its execution 48 or 64).
+      const uint32_t lead = elect_one() ? 1u : 0u;
+      const uint32_t idesc_qk = instr_desc(QK_BF16, QK_BF16, 0, BM, BN / 2);
+      const uint32_t idesc_pv = instr_desc(PV_BF16, PV_BF16, 1, BM, D);
+      const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV);
+      // Descriptors differ in the address field alone (bits [0, 14), 16-byte
+      // units; shared memory ends below 2^18), so one is another plus a
+      // constant: the issuing thread's instructions are on the S -> P chain.
+      const uint64_t qd0 = smem_desc(sQa, 16, 1024, 2u), kd0 = smem_desc(sKa, 16, 1024, 2u);
+      const uint64_t vd0 = smem_desc(sVa, C::BOXB, 1024, 2u);
+      // S of map t, keys [64 half, +64) of the K tile in stage ks
+      auto issue_qk = [&](int t, int ks, int half, int buf) {
+        const uint64_t kd = kd0 + static_cast<uint32_t>(ks * (C::TB / 16) + half * (64 * 128 / 16));
 #pragma unroll
-          for (int kk = 0; kk < DM / 16; ++kk) {
-            const uint32_t at = t * DM * 2 + kk * 32;          // byte of the row
-            const uint32_t off = at / 128 * C::BOXB + at % 128;
-            mma_f16_ss(tmem + col_s(t), smem_desc(sQa + off, 16, 1024, 2u),
-                       smem_desc(sKa + ks * C::TB + off, 16, 1024, 2u), idesc_qk, kk > 0);
-          }
-          any_mma = true;
-        };
-        auto issue_pv = [&](int t, int vs, bool acc) {
-#pragma unroll
-          for (int kk = 0; kk < BN / 16; ++kk)
-            mma_f16_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8,
-                       smem_desc(sVa + vs * C::TB + kk * 16 * 128, C::BOXB, 1024, 2u), idesc_pv, acc || kk > 0);
-          if constexpr (KIND == kBf16Split) {
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)               // the low parts, in the columns behind
-              mma_f16_ts(tmem + col_o(t), tmem + col_s(t) + 64 + kk * 8,
-                         smem_desc(sVa + vs * C::TB + kk * 16 * 128, C::BOXB, 1024, 2u), idesc_pv, 1);
-          }
-        };
-        bool ok = mbar_wait(&bar->q_full, 0, ctl) && mbar_wait(&bar->k_full[0], 0, ctl);
-        if (ok) {
-          tc_fence_after();
-          for (int t = 0; t < 2; ++t) {
-            issue_qk(t, 0);
-            mma_commit(&bar->s_full[t]);
-          }
-          mma_commit(&bar->k_empty[0]);
+        for (int kk = 0; kk < DM / 16; ++kk) {
+          const uint32_t at = t * DM * 2 + kk * 32;          // byte of the row
+          const uint32_t off = (at / 128 * C::BOXB + at % 128) / 16;
+          mma_ss_if(lead, tmem + col_s(t, buf), qd0 + off, kd + off, idesc_qk, kk > 0);
         }
-        for (int j = 0; j < n_kv && ok; ++j) {
-          const int vs = j % C::VS, ks = (j + 1) % C::KS;
-          const bool more = j + 1 < n_kv;
-          ok = mbar_wait(fix ? &bar->v_ready[vs] : &bar->v_full[vs], (j / C::VS) & 1, ctl);
-          for (int t = 0; t < 2 && ok; ++t) {
-            ok = mbar_wait(&bar->p_full[t], j & 1, ctl);
+      };
+      auto issue_pv = [&](int t, int vs, int half, int buf, bool acc) {
+        const uint64_t vd = vd0 + static_cast<uint32_t>(vs * (C::TB / 16) + half * (64 * 128 / 16));
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_if(lead, tmem + col_o(t), tmem + col_s(t, buf) + kk * 8, vd + kk * 128, idesc_pv, acc || kk > 0);
+        if constexpr (KIND == kBf16Split) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)                     // the low parts, in the columns behind
+            mma_ts_if(lead, tmem + col_o(t), tmem + col_s(t, buf) + 32 + kk * 8, vd + kk * 128, idesc_pv, 1);
+        }
+      };
+      int nq = 0, nk = 0, nv = 0;                     // segments, K tiles, V tiles so far
+      uint32_t idx = 0, p_phase = 0;                  // S commits of the CTA; parity bits of p_full
+      Segment s;
+      bool ok = true;
+      for (Walk walk(p, share); ok && walk.next(p, share, s);) {
+        if (s.n_kv == 0) continue;
+        const int n = s.n_half;
+        const bool fix = fixes(s);
+        ok = warp_wait(&bar->q_full, nq & 1, ctl) && warp_wait(&bar->k_full[nk % C::KS], (nk / C::KS) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after();
+        // Every S buffer hand-over is one commit: of halves 0 and 1 here,
+        // of half i + 2 behind P.V of half i -- also where there is no such
+        // half, so that S commit n + 1 proves the last P.V done.
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (i < n) issue_qk(t, nk % C::KS, i, (idx + i) & 1);
+            commit_if(lead, &bar->s_full[t][(idx + i) & 1]);
+          }
+        }
+        commit_if(lead, &bar->k_empty[nk % C::KS]);
+        ++nk;
+        if (n <= 2) commit_if(lead, &bar->q_empty);
+        int vs = nv % C::VS, ks = nk % C::KS;
+        uint32_t v_par = (nv / C::VS) & 1, k_par = (nk / C::KS) & 1;
+#pragma unroll 1
+        for (int i = 0; i < n && ok; ++i) {
+          const int buf = (idx + i) & 1, half = i & 1;
+          const bool more = i + 2 < n, v_last = half || i + 1 == n;
+          if (!half) {
+            ok = warp_wait(fix ? &bar->v_ready[vs] : &bar->v_full[vs], v_par, ctl) &&
+                 (!more || warp_wait(&bar->k_full[ks], k_par, ctl));
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            ok = warp_wait(&bar->p_full[t][buf], (p_phase >> buf) & 1, ctl);
             if (!ok) break;
             tc_fence_after();
-            issue_pv(t, vs, j > 0);
-            if (t == 1) mma_commit(&bar->v_empty[vs]);
-            if (more) {
-              if (t == 0) {
-                ok = mbar_wait(&bar->k_full[ks], ((j + 1) / C::KS) & 1, ctl);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              issue_qk(t, ks);
-              mma_commit(&bar->s_full[t]);
-              if (t == 1) mma_commit(&bar->k_empty[ks]);
-            } else {
-              mma_commit(&bar->o_final[t]);
-            }
+            issue_pv(t, vs, half, buf, i > 0);
+            if (more) issue_qk(t, ks, half, buf);
+            commit_if(lead, &bar->s_full[t][buf]);
           }
+          if (!ok) break;
+          p_phase ^= 1u << buf;
+          if (v_last) {
+            commit_if(lead, &bar->v_empty[vs]);
+            ++nv;
+            if (++vs == C::VS) { vs = 0; v_par ^= 1; }
+          }
+          if (more && (half || i + 3 == n)) {         // the K tile's last half
+            commit_if(lead, &bar->k_empty[ks]);
+            ++nk;
+            if (++ks == C::KS) { ks = 0; k_par ^= 1; }
+          }
+          if (i + 3 == n) commit_if(lead, &bar->q_empty);  // the segment's last Q.K^T
         }
-        if (any_mma) {
-          mma_commit(&bar->mma_final);
-          drain_wait(&bar->mma_final, 0, ctl);
+        idx += n + 2;
+        ++nq;
+      }
+      // the softmax warps wait for the last S commit of every segment; an
+      // aborted walk gives the products in flight time to end
+      if (*ctl.abort) {
+        const uint64_t t = globaltimer_ns();
+        while (globaltimer_ns() - t < 1000000ull) {
         }
       }
-    } else if (warp == kMaskWarp && fix) {
-      for (int j = 0; j < n_kv; ++j) {
-        const int vs = j % C::VS, key0 = (t0 + j) * BN;
-        bool drop[4];                                   // keys key0 + 32 w + lane
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int key = key0 + 32 * w + lane;
-          drop[w] = key < p.S_kv && (key >= len || (mask != nullptr && __ldg(mask + key) == 0));
-        }
-        if (!warp_wait(&bar->v_full[vs], (j / C::VS) & 1, ctl)) break;
-        uint8_t* tile = sV + vs * C::TB;
-        bool wrote = false;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t todo = __ballot_sync(0xffffffffu, drop[w]);
-          wrote = wrote || todo != 0;
-          // a row is 128 bytes of each box, wherever the swizzle put its pieces
-          while (todo != 0) {
-            const int r = 32 * w + __ffs(todo) - 1;
-            todo &= todo - 1;
-#pragma unroll
-            for (int x = 0; x < C::NBOX; ++x)
-              *reinterpret_cast<uint32_t*>(tile + x * C::BOXB + r * 128 + lane * 4) = 0u;
+    } else if (warp == kMaskWarp && KIND != kBf16WideV && (p.key_mask != nullptr || p.kv_len != nullptr)) {
+      int nv = 0;
+      Segment s;
+      bool ok = true;
+      for (Walk walk(p, share); ok && walk.next(p, share, s);) {
+        const bool fix = fixes(s);
+        const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(s.b) * p.S_kv : nullptr;
+        for (int j = 0; j < s.n_kv; ++j, ++nv) {
+          const int vs = nv % C::VS, key0 = (s.t0 + j) * BN;
+          if (!fix) {
+            // keep v_ready's phase with the stage's
+            ok = warp_wait(&bar->v_full[vs], (nv / C::VS) & 1, ctl);
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&bar->v_ready[vs]);
+            continue;
           }
+          bool drop[4];                                 // keys key0 + 32 w + lane
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int key = key0 + 32 * w + lane;
+            drop[w] = key < p.S_kv && (key >= s.len || (mask != nullptr && __ldg(mask + key) == 0));
+          }
+          ok = warp_wait(&bar->v_full[vs], (nv / C::VS) & 1, ctl);
+          if (!ok) break;
+          uint8_t* tile = sV + vs * C::TB;
+          bool wrote = false;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t todo = __ballot_sync(0xffffffffu, drop[w]);
+            wrote = wrote || todo != 0;
+            // a row is 128 bytes of each box, wherever the swizzle put its pieces
+            while (todo != 0) {
+              const int r = 32 * w + __ffs(todo) - 1;
+              todo &= todo - 1;
+#pragma unroll
+              for (int x = 0; x < C::NBOX; ++x)
+                *reinterpret_cast<uint32_t*>(tile + x * C::BOXB + r * 128 + lane * 4) = 0u;
+            }
+          }
+          if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->v_ready[vs]);
         }
-        if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->v_ready[vs]);
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs_softmax<D>()));
     const int t = warp >> 2;                            // map of this warpgroup
     const int row = (warp & 3) * 32 + lane;             // TMEM lane == row in the tile
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lane_base + col_s(t), to = tmem + lane_base + col_o(t);
-    const int r = rt * BM + row;                        // row of the group
-    const bool live = r < p.R;
-    const bool warp_live = rt * BM + (warp & 3) * 32 < p.R;
-    const int head = gi * p.hpg + (live ? r / p.S_q : 0), s_q = live ? r % p.S_q : 0;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t to = lane_base + col_o(t);
     const float c_j = p.scale_log2;
-    float m_run = -INFINITY, l_run = 0.f;
+    const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
+    uint32_t idx = 0, ex_phase = 0;
+    Segment s;
     bool ok = true;
-    uint8_t mb[4] = {1, 1, 1, 1};
-    auto load_mask = [&](int kt) {
+    for (Walk walk(p, share); ok && walk.next(p, share, s);) {
+      const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(s.b) * p.S_kv : nullptr;
+      const int r = s.rt * BM + row;                    // row of the range
+      const bool live = r < p.R;
+      const bool warp_live = s.rt * BM + (warp & 3) * 32 < p.R;
+      const int head = s.gi * p.hpg + (live ? r / p.S_q : 0), s_q = live ? r % p.S_q : 0;
+      const int n = s.n_half, key0 = s.t0 * BN;
+      float m_run = -INFINITY, l_run = 0.f;
+      uint8_t mb[2] = {1, 1};
+      auto load_mask = [&](int i) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const int key = kt * BN + 32 * w + lane;
-        mb[w] = key < p.S_kv ? __ldg(mask + key) : 0;
-      }
-    };
-    if (mask != nullptr && n_kv > 0) load_mask(t0);
-    for (int j = 0; j < n_kv; ++j) {
-      const int kt = t0 + j;
-      uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-      if (mask != nullptr) {
-#pragma unroll
-        for (int w = 0; w < 4; ++w) keep[w] = __ballot_sync(0xffffffffu, mb[w] != 0);
-        if (j + 1 < n_kv) load_mask(kt + 1);
-      }
-      ok = warp_wait(&bar->s_full[t], j & 1, ctl);
-      if (!ok) break;
-      __syncwarp();
-      if (!warp_live) {                                 // rows past the last: nothing to compute
-        mbar_arrive(&bar->p_full[t]);
-        continue;
-      }
-      tc_fence_after();
-      float v[BN];
-      {
-        uint32_t raw[BN];
-        tmem_ld128(ts, raw);
-#pragma unroll
-        for (int e = 0; e < BN; ++e) v[e] = __uint_as_float(raw[e]);
-      }
-      const int valid = len - kt * BN;
-      if (valid < BN) {
-#pragma unroll
-        for (int e = 0; e < BN; ++e)
-          if (e >= valid) v[e] = -INFINITY;
-      }
-      if ((keep[0] & keep[1] & keep[2] & keep[3]) != ~0u) {
-#pragma unroll
-        for (int e = 0; e < BN; ++e)
-          if (!((keep[e >> 5] >> (e & 31)) & 1u)) v[e] = -INFINITY;
-      }
-      const float mx = row_max(v) * c_j;
-      const float m_new = fmaxf(m_run, mx);
-      float alpha = 1.f;
-      const bool resc = (m_new - m_run) > kRescaleThreshold;
-      if (resc) {
-        alpha = ex2_approx(m_run - m_new);
-        m_run = m_new;
-        l_run *= alpha;
-      }
-      __syncwarp();
-      if (j > 0 && __any_sync(0xffffffffu, resc)) {
-        // O_t is stable here: PV_t(j-1) completed before S_t(j) was signalled
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(to + c * 32, o);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-          tmem_st32(to + c * 32, o);
+        for (int w = 0; w < 2; ++w) {
+          const int key = key0 + i * 64 + 32 * w + lane;
+          mb[w] = key < p.S_kv ? __ldg(mask + key) : 0;
         }
-      }
-      // no key so far: every probability is exp2(-inf) = 0
-      const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
-      const float2 c2 = make_float2(c_j, c_j), nm2 = make_float2(neg_m, neg_m);
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
+      };
+      if (mask != nullptr && n > 0) load_mask(0);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const uint32_t at = idx + i, buf = at & 1;
+        uint32_t keep[2] = {~0u, ~0u};
+        if (mask != nullptr) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
+          for (int w = 0; w < 2; ++w) keep[w] = __ballot_sync(0xffffffffu, mb[w] != 0);
+          if (i + 1 < n) load_mask(i + 1);
+        }
+        ok = warp_wait(&bar->s_full[t][buf], (at >> 1) & 1, ctl);
+        if (!ok) break;
+        if (!warp_live) {                               // rows past the last: nothing to compute
+          if (lane == 0) mbar_arrive(&bar->p_full[t][buf]);
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t ts = lane_base + col_s(t, buf);
+        float v[64];
+        {
+          uint32_t raw[64];
+          tmem_ld64(ts, raw);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) v[e] = __uint_as_float(raw[e]);
+        }
+        const int valid = s.len - key0 - i * 64;
+        if (valid < 64) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (e >= valid) v[e] = -INFINITY;
+        }
+        if ((keep[0] & keep[1]) != ~0u) {
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (!((keep[e >> 5] >> (e & 31)) & 1u)) v[e] = -INFINITY;
+        }
+        const float mx = row_max(v) * c_j;
+        const float m_new = fmaxf(m_run, mx);
+        float alpha = 1.f;
+        const bool resc = (m_new - m_run) > kRescaleThreshold;
+        if (resc) {
+          alpha = ex2_approx(m_run - m_new);
+          m_run = m_new;
+          l_run *= alpha;
+        }
+        __syncwarp();
+        if (i > 0 && __any_sync(0xffffffffu, resc)) {
+          // S commit i + 1 proves P.V of half i - 1 done: O_t is stable until
+          // this half's P is handed over
+          ok = warp_wait(&bar->s_full[t][buf ^ 1], ((at + 1) >> 1) & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(to + c * 32, o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(to + c * 32, o);
+          }
+        }
+        // no key so far: every probability is exp2(-inf) = 0
+        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+        const float2 c2 = make_float2(c_j, c_j), nm2 = make_float2(neg_m, neg_m);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
         uint32_t pk[32], lo[KIND == kBf16Split ? 32 : 1];
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
-          const int e = half * 64 + 2 * c;
+          const int e = 2 * c;
           const float2 x0 = __ffma2_rn(make_float2(v[e + 0], v[e + 1]), c2, nm2);
           const float2 x1 = __ffma2_rn(make_float2(v[e + 2], v[e + 3]), c2, nm2);
           const float2 e0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
@@ -515,28 +725,30 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                       e1.y - __uint_as_float(pk[c + 1] & 0xFFFF0000u));
           }
         }
-        tmem_st32(ts + half * 32, pk);
-        if constexpr (KIND == kBf16Split) tmem_st32(ts + 64 + half * 32, lo);
+        tmem_st32(ts, pk);
+        if constexpr (KIND == kBf16Split) tmem_st32(ts + 32, lo);
+        l_run += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        // one arrival per warp: 128 to one address take turns
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->p_full[t][buf]);
       }
-      l_run += (acc0.x + acc0.y) + (acc1.x + acc1.y);
-      tc_fence_before();
-      mbar_arrive(&bar->p_full[t]);
-    }
-    if (ok && n_kv > 0) ok = warp_wait(&bar->o_final[t], 0, ctl);
-    __syncwarp();
-    tc_fence_after();
-    float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-    if constexpr (KIND == kBf16WideV)                   // undo V's power of two
-      inv *= pow2(v_exponent(__ldg(p.v_amax + static_cast<size_t>(b) * p.H_kv + kvh)));
-    const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
-    const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
-    const size_t rg = (static_cast<size_t>(b) * p.H + head) * p.S_q + s_q;
-    if (p.splits > 1) {
-      // this split's normalised output and log-sum-exp of its map
-      if (ok && warp_live) {
-        const size_t at = (static_cast<size_t>(sp) * 2 + t) * rows + rg;
-        float* dst = p.part_o + at * D;
-        if (n_kv > 0) {
+      if (!ok) break;
+      if (n > 0) {
+        ok = warp_wait(&bar->s_full[t][(idx + n + 1) & 1], ((idx + n + 1) >> 1) & 1, ctl);
+        if (!ok) break;
+        idx += n + 2;
+      }
+      tc_fence_after();
+      float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      if constexpr (KIND == kBf16WideV)                 // undo V's power of two
+        inv *= pow2(v_exponent(__ldg(p.v_amax + static_cast<size_t>(s.b) * p.H_kv + kv_head(s.gi))));
+      const float lse2 = l_run == 0.f ? -INFINITY : m_run + __log2f(l_run);
+      if (!s.whole) {
+        // this part's normalised output and log-sum-exp of its map
+        const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.from_start ? 1 : 0);
+        if (warp_live) {
+          float* dst = p.part_o + ((slot * 2 + t) * BM + row) * D;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -550,24 +762,24 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                 __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
             }
           }
+          if (live) p.part_l[(slot * 2 + t) * BM + row] = lse2;
         }
-        // a split without keys leaves its output unwritten: weight 0 by its -inf
-        if (live) p.part_l[at] = lse2;
+        tc_fence_before();                              // before the next segment's P.V overwrites O_t
+        continue;
       }
-    } else {
-      const float lam = ok && live ? lambda_of(p, head, DM) : 0.f;
+      const float lam = live ? lambda_of(p, head, DM) : 0.f;
       sL[t * BM + row] = inv;
       tc_fence_before();
       mbar_arrive(&bar->exchange[0]);
-      ok = warp_wait(&bar->exchange[0], 0, ctl) && ok;
+      ok = warp_wait(&bar->exchange[0], ex_phase, ctl);
+      if (!ok) break;
       tc_fence_after();
       // channels [t * D / 2, +D / 2) of the row
       const float w1 = sL[row], w2 = -lam * sL[BM + row];
       float o[DM];
       float sq = 0.f;
-      __syncwarp();
-      if (n_kv > 0 && ok) {
-        const uint32_t o1 = tmem + lane_base + col_o(0) + t * DM, o2 = tmem + lane_base + col_o(1) + t * DM;
+      if (n > 0) {
+        const uint32_t o1 = lane_base + col_o(0) + t * DM, o2 = lane_base + col_o(1) + t * DM;
 #pragma unroll
         for (int c = 0; c < DM; c += 32) {
           uint32_t x[32], y[32];
@@ -583,10 +795,14 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
         for (int e = 0; e < DM; ++e) o[e] = 0.f;
       }
+      // also the point after which neither O is read any more
+      sSq[t * BM + row] = sq;
+      tc_fence_before();
+      mbar_arrive(&bar->exchange[1]);
+      ok = warp_wait(&bar->exchange[1], ex_phase, ctl);
+      if (!ok) break;
+      ex_phase ^= 1u;
       if (p.norm_w != nullptr) {
-        sSq[t * BM + row] = sq;
-        mbar_arrive(&bar->exchange[1]);
-        ok = warp_wait(&bar->exchange[1], 0, ctl) && ok;
         const float f = rsqrtf((sSq[row] + sSq[BM + row]) * (1.f / D) + p.eps) * (1.f - p.lambda_init);
 #pragma unroll
         for (int e = 0; e < DM; e += 4) {
@@ -597,8 +813,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           o[e + 3] *= f * w.w;
         }
       }
-      if (ok && live) {
-        __nv_bfloat16* dst = p.o + ((static_cast<size_t>(b) * p.S_q + s_q) * p.H + head) * D + t * DM;
+      if (live) {
+        __nv_bfloat16* dst = p.o + ((static_cast<size_t>(s.b) * p.S_q + s_q) * p.H + head) * D + t * DM;
         uint32_t w[DM / 2];
 #pragma unroll
         for (int e = 0; e < DM / 2; ++e) w[e] = pack_x2<true>(o[2 * e], o[2 * e + 1]);
@@ -614,7 +830,9 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int e = 0; e < DM / 2; e += 4)
             *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
         }
-        if (p.lse != nullptr) p.lse[static_cast<size_t>(t) * rows + rg] = lse2 * 0.69314718055994531f;
+        if (p.lse != nullptr)
+          p.lse[static_cast<size_t>(t) * rows + (static_cast<size_t>(s.b) * p.H + head) * p.S_q + s_q] =
+              lse2 * 0.69314718055994531f;
       }
     }
   }
@@ -629,18 +847,39 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-// Merge of the splits, one warp per query row: each map's outputs weighted by
-// 2^(lse_s - lse), then the difference and the norm.
+// Merge of the items that several CTAs shared, one warp per query row: each
+// map's parts weighted by 2^(lse_part - lse), then the difference and the
+// norm.  blockIdx.x + 1 = a CTA of the walk; the first whose share starts
+// inside an item answers for that item.
 template <int D>
-__global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p) {
+__global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int ctas) {
   constexpr int E = D / 32;                             // channels per lane
   const int lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  const int cta = blockIdx.x + 1;
+  const long long total = shared_prefix(p, p.B);
+  const long long g = share_start(total, cta, ctas);
+  if (g >= total) return;
+  long long item;
+  int off;
+  locate(p, g, item, off);
+  if (off == 0 || share_start(total, cta - 1, ctas) > g - off) return;
+  const int per = p.n_groups * p.n_rt;
+  const int b = static_cast<int>(item / per), gi = static_cast<int>(item / p.n_rt % p.n_groups);
+  const int r = static_cast<int>(item % p.n_rt) * BM + row;
+  if (r >= p.R) return;
+  const long long end = g - off + tiles_of(p, b);       // the item's last tile + 1
+  int last = cta;                                       // the last CTA that has a part of it
+  while (last + 1 < ctas && share_start(total, last + 1, ctas) < end) ++last;
+  const int parts = last - cta + 2;
+  const int head = gi * p.hpg + r / p.S_q, s_q = r % p.S_q;
   const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
-  const size_t rg = static_cast<size_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (rg >= rows) return;
-  const int s_q = static_cast<int>(rg % p.S_q);
-  const size_t bh = rg / p.S_q;
-  const int head = static_cast<int>(bh % p.H), b = static_cast<int>(bh / p.H);
+  const size_t rg = (static_cast<size_t>(b) * p.H + head) * p.S_q + s_q;
+  // part 0 is the end of CTA cta - 1's share, part i the start of cta + i - 1's
+  auto part_at = [&](int i, int t) {
+    const size_t slot = i == 0 ? 2 * static_cast<size_t>(cta - 1) + 1 : 2 * static_cast<size_t>(cta + i - 1);
+    return (slot * 2 + t) * BM + row;
+  };
   float a1 = 0.f, a2 = 0.f;
   const size_t plane = static_cast<size_t>(p.H) * (D / 2);
   for (int i = lane; i < D / 2; i += 32) {
@@ -660,18 +899,18 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p) {
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     float mx = -INFINITY;
-    for (int s = 0; s < p.splits; ++s) {
-      const float l = p.part_l[(static_cast<size_t>(s) * 2 + t) * rows + rg];
+    for (int s = 0; s < parts; ++s) {
+      const float l = p.part_l[part_at(s, t)];
       mx = l > mx || l != l ? l : mx;                   // a NaN stays
     }
     float acc[E], tot = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     if (mx != -INFINITY) {
-      for (int s = 0; s < p.splits; ++s) {
-        const size_t at = (static_cast<size_t>(s) * 2 + t) * rows + rg;
+      for (int s = 0; s < parts; ++s) {
+        const size_t at = part_at(s, t);
         const float l = p.part_l[at];
-        if (l == -INFINITY) continue;                   // no keys: its output was not written
+        if (l == -INFINITY) continue;
         const float w = ex2_approx(l - mx);
         tot += w;
         const float* src = p.part_o + at * D + lane * E;
@@ -716,11 +955,10 @@ cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorM
     widen_v_kernel<D, false><<<grid, 256, 0, st>>>(p);
     widen_v_kernel<D, true><<<grid, 256, 0, st>>>(p);
   }
-  const long long items = static_cast<long long>(p.B) * p.n_groups * p.splits * p.n_rt;
-  kern<<<static_cast<unsigned>(items), kThreads, C::SMEM, st>>>(tq, tk, tv, p);
-  if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
-  const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
-  diff_merge_kernel<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, st>>>(p);
+  kern<<<p.ctas, kThreads, C::SMEM, st>>>(tq, tk, tv, p);
+  if ((e = cudaGetLastError()) != cudaSuccess || !p.merge) return e;
+  const dim3 grid(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>(((p.R < BM ? p.R : BM) + 3) / 4));
+  diff_merge_kernel<D><<<grid, 128, 0, st>>>(p, p.ctas);
   return cudaGetLastError();
 }
 
@@ -733,14 +971,36 @@ cudaError_t launch_d(const DiffParams& p, bool in_bf16, const CUtensorMap& tq, c
 
 }  // namespace
 
-// Splits of the keys: none while the items alone give every SM a CTA.
-int diff_splits(long long items, int S_kv) {
-  const int tiles = (S_kv + BN - 1) / BN;
-  if (items >= 148 || tiles < 8) return 1;
-  long long s = 444 / items;
-  if (s > tiles / 4) s = tiles / 4;
-  if (s > 64) s = 64;
-  return s < 1 ? 1 : static_cast<int>(s);
+// How the items are walked: pure host arithmetic.
+DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms) {
+  const long long tiles = (S_kv + BN - 1) / BN;
+  DiffWalk w{};
+  if (items < sms) {
+    // fewer items than SMs: cut them where a CTA still gets a few key tiles
+    w.ctas = static_cast<int>(items);
+    if (tiles >= 8) {
+      const long long c = items * tiles / 4;
+      w.ctas = static_cast<int>(c < sms ? c : sms);
+      w.items_whole = 0;
+      w.merge = w.ctas > 1;
+      if (w.ctas < items) w.ctas = static_cast<int>(items);
+      return w;
+    }
+    w.items_whole = items;
+    return w;
+  }
+  w.ctas = sms;
+  w.items_whole = items;
+  if (tiles >= 8) {
+    // One row tile per range: every key tile is read once, in any order.
+    // Otherwise the last wave, where the key tiles it saves each CTA (about
+    // 1.5 us each) exceed the parts' way through memory (about 12 us).
+    const long long rest = items % sms;
+    if (n_rt == 1) w.items_whole = 0;
+    else if (rest > 0 && (sms - rest) * tiles > 8ll * sms) w.items_whole = items - rest;
+  }
+  w.merge = w.items_whole < items;
+  return w;
 }
 
 // Whether bf16 operands get an fp16 copy of V: worth its three passes over V

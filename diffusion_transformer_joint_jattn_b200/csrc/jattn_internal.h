@@ -201,7 +201,10 @@ cudaError_t launch_linear(LinearParams p, const LinearPlan& plan, bool tma, cons
 struct DiffParams {
   int B, H, H_kv, S_q, S_kv;
   int n_groups, hpg, R, n_rt;   // heads and rows of a range, its 128-row tiles
-  int splits;                   // parts the keys are walked in (workspace when > 1)
+  long long items;              // B * n_groups * n_rt
+  long long items_whole;        // the items below this number are walked whole, the others shared by all CTAs
+  int ctas;                     // of the walk
+  int merge;                    // items are shared: parts to merge
   float scale_log2;
   const float* lam;             // [4][H][d / 2]
   float lambda_init;
@@ -211,8 +214,8 @@ struct DiffParams {
   const uint8_t* key_mask;      // [B][S_kv], nonzero = takes part, or null
   __nv_bfloat16* o;             // [B][S_q][H][d]
   float* lse;                   // [2][B][H][S_q] or null
-  float* part_o;                // [splits][2][B*H*S_q][d]
-  float* part_l;                // [splits][2][B*H*S_q], log2 units
+  float* part_o;                // [2 * ctas][2][128][d]: the parts of shared items
+  float* part_l;                // [2 * ctas][2][128], log2 units
   const __nv_bfloat16* v;       // with v16: the bf16 values it is made from, and their strides in elements
   int64_t v_stride[3];          //   over (batch entry, head, token)
   __half* v16;                  // null, or [B][H_kv][S_kv][d]: fp16 copy of v, divided by a power of two per head
@@ -220,7 +223,11 @@ struct DiffParams {
   uint32_t* status;
   uint64_t timeout_ns;
 };
-int diff_splits(long long items, int S_kv);
+struct DiffWalk {
+  long long items_whole;
+  int ctas, merge;
+};
+DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms);
 bool diff_widens_v(int n_rt);
 // The maps describe (d, rows, heads or ranges, batch) with boxes of 64 x 128.
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,

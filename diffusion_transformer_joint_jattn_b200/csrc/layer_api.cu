@@ -45,7 +45,9 @@ bool heads_map(CUtensorMap* m, const void* base, int d, int64_t rows, int64_t he
 // Row ranges of a call: the rows of the heads that share a K/V head form one
 // range when they are equally spaced in memory.
 struct DiffRanges {
-  int n_groups, hpg, R, n_rt, splits;
+  int n_groups, hpg, R, n_rt;
+  int64_t items;
+  jattn::DiffWalk walk;
   int64_t row_stride, group_stride;
 };
 
@@ -71,8 +73,8 @@ jattn_status diff_ranges(const jattn_diff_shape* s, DiffRanges* r) {
   r->R = static_cast<int>(rows);
   r->row_stride = s->S_q == 1 ? s->q_stride[1] : s->q_stride[2];
   r->group_stride = r->hpg * s->q_stride[1];
-  const int64_t items = static_cast<int64_t>(s->B) * r->n_groups * r->n_rt;
-  r->splits = items > 0 ? jattn::diff_splits(items, s->S_kv) : 1;
+  r->items = static_cast<int64_t>(s->B) * r->n_groups * r->n_rt;
+  r->walk = jattn::diff_walk(r->items, r->n_rt, s->S_kv, jattn::device_sm_count());
   return JATTN_OK;
 }
 
@@ -86,10 +88,9 @@ DiffLayout diff_layout(const jattn_diff_shape* s, const DiffRanges& r, bool in_b
   DiffLayout L{};
   size_t off = 0;
   auto seg = [&](size_t bytes) { const size_t at = off; off += (bytes + 255) / 256 * 256; return at; };
-  if (r.splits > 1) {
-    const size_t rows = static_cast<size_t>(s->B) * s->H * s->S_q;
-    L.part_o = seg(r.splits * 2 * rows * s->d * 4);
-    L.part_l = seg(r.splits * 2 * rows * 4);
+  if (r.walk.merge) {
+    L.part_o = seg(static_cast<size_t>(r.walk.ctas) * 4 * 128 * s->d * 4);
+    L.part_l = seg(static_cast<size_t>(r.walk.ctas) * 4 * 128 * 4);
   }
   if (in_bf16 && jattn::diff_widens_v(r.n_rt) && s->S_kv > 0) {
     L.v16 = seg(static_cast<size_t>(s->B) * s->H_kv * s->S_kv * s->d * 2);
@@ -250,8 +251,6 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   const size_t need = L.total;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return JATTN_ERR_INVALID_ARG;
   if (need > 0 && !aligned(workspace, 256)) return JATTN_ERR_ALIGNMENT;
-  const int64_t items = static_cast<int64_t>(s->B) * r.n_groups * r.n_rt * r.splits;
-  if (items > INT32_MAX) return JATTN_ERR_INVALID_ARG;
   jattn::DiffParams p{};
   p.B = s->B;
   p.H = s->H;
@@ -262,7 +261,10 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   p.hpg = r.hpg;
   p.R = r.R;
   p.n_rt = r.n_rt;
-  p.splits = r.splits;
+  p.items = r.items;
+  p.items_whole = r.walk.items_whole;
+  p.ctas = r.walk.ctas;
+  p.merge = r.walk.merge;
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(0.5f * static_cast<float>(s->d));
   p.scale_log2 = scale * 1.4426950408889634f;
   p.lam = lam;
@@ -274,7 +276,7 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  if (r.splits > 1) {
+  if (r.walk.merge) {
     p.part_o = reinterpret_cast<float*>(ws + L.part_o);
     p.part_l = reinterpret_cast<float*>(ws + L.part_l);
   }

@@ -293,21 +293,22 @@ __device__ __forceinline__ void stage_plain(const uint16_t* g, int64_t ld, int64
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int k = k0 + 2 * lane;
   const bool in0 = k < K, in1 = k + 1 < K;
+  const int ka = in0 ? k : 0, kb = in1 ? k + 1 : 0;
   for (int r0 = warp; r0 < rows; r0 += 4 * RB) {
-    uint16_t lo[RB], hi[RB];
-    const uint16_t* src = g + (row0 + r0) * ld + k;
+    uint32_t lo[RB], hi[RB];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const bool row_in = r0 + 4 * i < rows && row0 + r0 + 4 * i < n_rows;
-      lo[i] = row_in && in0 ? __ldg(src + 4 * i * ld) : 0;
-      hi[i] = row_in && in1 ? __ldg(src + 4 * i * ld + 1) : 0;
+    for (int i = 0; i < RB; ++i) {                     // clamped, not skipped: no branch between the loads
+      const uint16_t* src = g + min(row0 + r0 + 4 * i, n_rows - 1) * ld;
+      lo[i] = __ldg(src + ka);
+      hi[i] = __ldg(src + kb);
     }
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
       const int r = r0 + 4 * i;
+      const bool row_in = row0 + r < n_rows;
       if (r < rows)
         *reinterpret_cast<uint32_t*>(dst + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2)) =
-            static_cast<uint32_t>(lo[i]) | (static_cast<uint32_t>(hi[i]) << 16);
+            (row_in && in0 ? lo[i] : 0u) | (row_in && in1 ? hi[i] << 16 : 0u);
     }
   }
 }
