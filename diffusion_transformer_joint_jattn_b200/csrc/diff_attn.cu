@@ -71,8 +71,8 @@ struct Cfg {
   static constexpr int KS = D == 128 ? 3 : 4;
   static constexpr int VS = D == 128 ? 3 : 4;
   static constexpr int EX = 4 * BM * 4;               // row sums and squares of both maps
-  static constexpr int SLACK = 704;                   // to align the tiles to 1024 bytes
-  static constexpr int SMEM = (1 + KS + VS) * TB + EX + 320 + SLACK;
+  static constexpr int SLACK = 640;                   // to align the tiles to 1024 bytes
+  static constexpr int SMEM = (1 + KS + VS) * TB + EX + 384 + SLACK;
 };
 
 // This CTA's run of the shared items' key tiles: from tile `off` of item
@@ -88,6 +88,7 @@ struct __align__(8) Bars {
   uint64_t v_full[4], v_empty[4], v_ready[4];
   uint64_t s_full[2][2], p_full[2][2];                // [map][buffer]
   uint64_t exchange[2];
+  uint64_t turn[2][4];                                // [map][warp]
   Share share;
   uint32_t tmem_base;
   uint32_t abort;
@@ -96,6 +97,12 @@ struct __align__(8) Bars {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
   const bool ok = mbar_wait(bar, parity, ctl);
   return __all_sync(0xffffffffu, ok);
+}
+// 32 TMEM columns per lane; tmem_wait_st waits for it.
+__device__ __forceinline__ void tmem_st32_issue(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
 }
 // The MMA and commit instructions by the lane with `lead` set.
 __device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -372,7 +379,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   float* sL = reinterpret_cast<float*>(sV + C::VS * C::TB);   // [2][BM] 1 / l
   float* sSq = sL + 2 * BM;                                   // [2][BM] sums of squares
   Bars* bar = reinterpret_cast<Bars*>(sSq + 2 * BM);
-  static_assert(sizeof(Bars) <= 320, "room for the barriers");
+  static_assert(sizeof(Bars) <= 384, "room for the barriers");
 
   // from one lane, so that the compiler sees the roles' branches as uniform
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
@@ -395,6 +402,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
       mbar_init(&bar->exchange[t], 2 * BM);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&bar->turn[0][i], 1);
     bar->abort = 0;
     fence_mbarrier_init();
   }
@@ -622,7 +630,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     const uint32_t to = lane_base + col_o(t);
     const float c_j = p.scale_log2;
     const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
-    uint32_t idx = 0, ex_phase = 0;
+    uint32_t idx = 0, ex_phase = 0, turns = 0;
     Segment s;
     bool ok = true;
     for (Walk walk(p, share); ok && walk.next(p, share, s);) {
@@ -702,6 +710,12 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             tmem_st32(to + c * 32, o);
           }
         }
+        // The two warps of a scheduler (map 0's and map 1's of the same rows)
+        // take the exponential unit in turns: left to themselves they fall into
+        // step, want it at the same time and leave it idle at the same time.
+        ok = warp_wait(&bar->turn[t][warp & 3], (turns ^ (t ^ 1)) & 1, ctl);
+        if (!ok) break;
+        ++turns;
         // no key so far: every probability is exp2(-inf) = 0
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
         const float2 c2 = make_float2(c_j, c_j), nm2 = make_float2(neg_m, neg_m);
@@ -725,8 +739,10 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                       e1.y - __uint_as_float(pk[c + 1] & 0xFFFF0000u));
           }
         }
-        tmem_st32(ts, pk);
-        if constexpr (KIND == kBf16Split) tmem_st32(ts + 32, lo);
+        tmem_st32_issue(ts, pk);
+        if constexpr (KIND == kBf16Split) tmem_st32_issue(ts + 32, lo);
+        if (lane == 0) mbar_arrive(&bar->turn[t ^ 1][warp & 3]);
+        tmem_wait_st();
         l_run += (acc0.x + acc0.y) + (acc1.x + acc1.y);
         // one arrival per warp: 128 to one address take turns
         tc_fence_before();
