@@ -52,12 +52,15 @@ constexpr int BN = 128;                // keys per tile
 constexpr int kMmaWarp = 8, kProducerWarp = 9, kMaskWarp = 10, kShareWarp = 11;
 constexpr int kThreads = 384;
 // Register split after setmaxnreg, together the 384 x 168 the block launches
-// with; each leaves the softmax and the single-thread roles without spills
-// (-Xptxas -v).
+// with: the fewest spills (-Xptxas -v: at most 16 bytes, outside the walks).
 template <int D> __host__ __device__ constexpr uint32_t regs_softmax() { return D == 128 ? 208u : 216u; }
 template <int D> __host__ __device__ constexpr uint32_t regs_other() { return (kThreads * 168u - 256u * regs_softmax<D>()) / 128u; }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 15.0f;   // log2 units; P <= 2^15 in 16 bits
+// Every kPolyEvery-th pair of exponentials is done on the FMA pipe: at 16896
+// tokens x 6 heads all on the exponential unit took 1310 us, every 8th pair
+// 1270, every 4th 1290, every 3rd 1286 (the chip is at its power limit there).
+constexpr int kPolyEvery = 8;
 
 __host__ __device__ constexpr uint32_t col_s(int t, int buf) { return static_cast<uint32_t>(t * 128 + buf * 64); }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(t) * 128u; }
@@ -97,6 +100,15 @@ struct __align__(8) Bars {
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtl& ctl) {
   const bool ok = mbar_wait(bar, parity, ctl);
   return __all_sync(0xffffffffu, ok);
+}
+// An arrival by the lane with `lead` set, without a branch.
+__device__ __forceinline__ void arrive_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];\n\t}\n"
+      ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
 }
 // 32 TMEM columns per lane; tmem_wait_st waits for it.
 __device__ __forceinline__ void tmem_st32_issue(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -161,9 +173,30 @@ __device__ __forceinline__ uint32_t pack_x2(float a, float b) {
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Two exponentials on the FMA pipe: 2^x = 2^n 2^f, n the nearest integer (by
+// adding and subtracting 1.5 * 2^23, whose low bits then hold n), f in [-1/2,
+// 1/2], 2^f by the degree-4 polynomial with value 1 at 0 that minimises the
+// largest relative error there (2.8e-6; coefficients by iteratively
+// reweighted least squares), n added to the exponent bits.  x is clamped at
+// -127, where the result is exactly 0.  NaN does not survive the bit
+// arithmetic: the caller sees to it.
+__device__ __forceinline__ float2 ex2_poly(float2 x) {
+  x = make_float2(fmaxf(x.x, -127.f), fmaxf(x.y, -127.f));
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  const float2 t = __fadd2_rn(x, magic);
+  const float2 n = __fadd2_rn(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+  float2 q = __ffma2_rn(f, make_float2(0x1.3a02ccp-7f, 0x1.3a02ccp-7f), make_float2(0x1.c9fc46p-5f, 0x1.c9fc46p-5f));
+  q = __ffma2_rn(q, f, make_float2(0x1.ec0378p-3f, 0x1.ec0378p-3f));
+  q = __ffma2_rn(q, f, make_float2(0x1.62e12cp-1f, 0x1.62e12cp-1f));
+  q = __ffma2_rn(q, f, make_float2(1.f, 1.f));
+  return make_float2(__uint_as_float(__float_as_uint(q.x) + (__float_as_uint(t.x) << 23)),
+                     __uint_as_float(__float_as_uint(q.y) + (__float_as_uint(t.y) << 23)));
+}
+// NaN if any value is one (max.f32 alone would drop it).
 __device__ __forceinline__ float row_max(const float (&v)[64]) {
   float a[21];
 #pragma unroll
@@ -171,7 +204,7 @@ __device__ __forceinline__ float row_max(const float (&v)[64]) {
   float c[7];
 #pragma unroll
   for (int i = 0; i < 7; ++i) c[i] = max3(a[3 * i], a[3 * i + 1], a[3 * i + 2]);
-  return max3(max3(c[0], c[1], c[2]), max3(c[3], c[4], c[5]), fmaxf(c[6], v[63]));
+  return max3(max3(c[0], c[1], c[2]), max3(c[3], c[4], c[5]), max3(c[6], v[63], v[63]));
 }
 
 // Keys of batch entry b (the length clamped into the cache).
@@ -662,7 +695,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         ok = warp_wait(&bar->s_full[t][buf], (at >> 1) & 1, ctl);
         if (!ok) break;
         if (!warp_live) {                               // rows past the last: nothing to compute
-          if (lane == 0) mbar_arrive(&bar->p_full[t][buf]);
+          arrive_if(lane == 0, &bar->p_full[t][buf]);
           continue;
         }
         tc_fence_after();
@@ -722,32 +755,27 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
         uint32_t pk[32], lo[KIND == kBf16Split ? 32 : 1];
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) {
-          const int e = 2 * c;
-          const float2 x0 = __ffma2_rn(make_float2(v[e + 0], v[e + 1]), c2, nm2);
-          const float2 x1 = __ffma2_rn(make_float2(v[e + 2], v[e + 3]), c2, nm2);
-          const float2 e0 = make_float2(ex2_approx(x0.x), ex2_approx(x0.y));
-          const float2 e1 = make_float2(ex2_approx(x1.x), ex2_approx(x1.y));
-          acc0 = __fadd2_rn(acc0, e0);
-          acc1 = __fadd2_rn(acc1, e1);
+        for (int c = 0; c < 32; ++c) {
+          const float2 x = __ffma2_rn(make_float2(v[2 * c], v[2 * c + 1]), c2, nm2);
+          const float2 e = c % kPolyEvery == kPolyEvery - 1 ? ex2_poly(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          if (c & 1) acc1 = __fadd2_rn(acc1, e);
+          else acc0 = __fadd2_rn(acc0, e);
           // P in V's type (the MMA wants one type); l sums the unrounded values
-          pk[c] = pack_x2<PV_BF16>(e0.x, e0.y);
-          pk[c + 1] = pack_x2<PV_BF16>(e1.x, e1.y);
-          if constexpr (KIND == kBf16Split) {
-            lo[c] = pack_x2<true>(e0.x - __uint_as_float(pk[c] << 16), e0.y - __uint_as_float(pk[c] & 0xFFFF0000u));
-            lo[c + 1] = pack_x2<true>(e1.x - __uint_as_float(pk[c + 1] << 16),
-                                      e1.y - __uint_as_float(pk[c + 1] & 0xFFFF0000u));
-          }
+          pk[c] = pack_x2<PV_BF16>(e.x, e.y);
+          if constexpr (KIND == kBf16Split)
+            lo[c] = pack_x2<true>(e.x - __uint_as_float(pk[c] << 16), e.y - __uint_as_float(pk[c] & 0xFFFF0000u));
         }
         tmem_st32_issue(ts, pk);
         if constexpr (KIND == kBf16Split) tmem_st32_issue(ts + 32, lo);
-        if (lane == 0) mbar_arrive(&bar->turn[t ^ 1][warp & 3]);
+        // passed earlier, among the last exponentials, it cost 3%
+        arrive_if(lane == 0, &bar->turn[t ^ 1][warp & 3]);
         tmem_wait_st();
         l_run += (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        if (mx != mx) l_run = mx;                       // NaN in, NaN out
         // one arrival per warp: 128 to one address take turns
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->p_full[t][buf]);
+        arrive_if(lane == 0, &bar->p_full[t][buf]);
       }
       if (!ok) break;
       if (n > 0) {
