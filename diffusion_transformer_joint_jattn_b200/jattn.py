@@ -620,36 +620,38 @@ _ACT_CODE = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3, "relu": 4}
 _ROTARY_LAYOUT = {"interleaved": 0, "half": 1}
 
 
-def _enqueue(dev, stream, inputs, call):
-    """``call(stream pointer)`` with ``dev`` current and the stream given (the
-    device's current one when None).  On a stream that is not the current one
-    the outputs are allocated for that stream, and the inputs are kept from
-    reuse until its work is done."""
-    if stream is None and dev.index == torch._C._cuda_getDevice():
-        return call(torch._C._cuda_getCurrentRawStream(dev.index))
+def _elsewhere(call, dev: int, stream, tensors):
+    """``call()`` with the tensors' device current and on ``stream`` (that
+    device's current one when None).  The outputs are allocated for that
+    stream, and the tensors are kept from reuse until its work is done."""
     with torch.cuda.device(dev):
         if stream is None or stream == torch.cuda.current_stream():
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call()
         with torch.cuda.stream(stream):
-            out = call(stream.cuda_stream)
-        for t in inputs:
+            out = call()
+        for t in tensors:
             if t is not None:
                 t.record_stream(stream)
         return out
 
 
-def _on(t, name: str, dev, dtypes):
-    """``t`` is a tensor on the CUDA device ``dev`` of one of ``dtypes``."""
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+def _float_check(t, name: str, dev: int, dtypes):
+    """``t`` is a tensor on CUDA device ``dev`` of one of ``dtypes``."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
 
 
-def _cuda_device(t, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.device
+def _plain_check(t, name: str, dev: int, dtypes, shape):
+    """As _float_check, and contiguous of that shape."""
+    if t.get_device() != dev or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} tensor of {' or '.join(str(d) for d in dtypes)} on "
+                         f"cuda:{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+_F32, _F64, _I32, _BYTES, _BF16 = (torch.float32,), (torch.float64,), (torch.int32,), (torch.uint8,), (torch.bfloat16,)
+_MASKS = (torch.bool, torch.uint8)
 
 
 def rotary_freqs(dim=None, theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -713,54 +715,73 @@ def rotary(q, k, pos, freqs, split: Optional[Sequence[int]] = None, layout: str 
     out: (q_out, k_out) of the inputs' shapes and any strides, which may be
     the inputs themselves; new contiguous tensors when None.
     Returns (q_out, k_out)."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: rotary(q, k, pos, freqs, split, layout, parts, scale, inverse, out), dev, stream,
+                          (q, k, pos, freqs, *(out or ())))
     lib = load()
-    dev = _cuda_device(q, "q")
-    xs = (q,) if k is None else (q, k)
     if q.dim() != 4:
         raise ValueError(f"q must be [B, S, H, d], got {tuple(q.shape)}")
-    B, S, _, d = q.shape
+    B, S, H, d = q.shape
     dtype = q.dtype
-    if dtype not in _FLOAT_CODE:
+    code = _FLOAT_CODE.get(dtype)
+    if code is None:
         raise ValueError(f"q must be bf16, fp16 or fp32, got {dtype}")
-    for name, t in zip(("q", "k"), xs):
-        if t.dim() != 4 or t.shape[0] != B or t.shape[1] != S or t.shape[3] != d:
-            raise ValueError(f"{name} must be [{B}, {S}, H, {d}], got {tuple(t.shape)}")
-        if t.dtype != dtype or t.device != dev:
-            raise ValueError(f"{name} must be {dtype} on {dev}, got {t.dtype} on {t.device}")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name}'s channels must be contiguous")
+    qs = q.stride()
+    if qs[3] != 1:
+        raise ValueError("q's channels must be contiguous")
+    if k is not None:
+        if k.dim() != 4 or k.shape[0] != B or k.shape[1] != S or k.shape[3] != d:
+            raise ValueError(f"k must be [{B}, {S}, H, {d}], got {tuple(k.shape)}")
+        if k.dtype != dtype or k.get_device() != dev:
+            raise ValueError(f"k must be {dtype} on cuda:{dev}, got {k.dtype} on {k.device}")
+        ks = k.stride()
+        if ks[3] != 1:
+            raise ValueError("k's channels must be contiguous")
     if layout not in _ROTARY_LAYOUT:
         raise ValueError(f"unknown layout {layout!r}")
-    if pos.dtype != torch.int32 or pos.device != dev or not pos.is_contiguous():
-        raise ValueError(f"pos must be a contiguous int32 tensor on {dev}")
+    if pos.dtype != torch.int32 or pos.get_device() != dev or not pos.is_contiguous():
+        raise ValueError(f"pos must be a contiguous int32 tensor on cuda:{dev}")
     want = (S,) if split is None else (S, 3)
-    if tuple(pos.shape) == (B, *want):
-        per_batch = pos[0].numel() if B > 1 else 0
-    elif tuple(pos.shape) == want:
+    if pos.shape == (B, *want):
+        per_batch = 0 if B == 1 else (S if split is None else 3 * S)
+    elif pos.shape == want:
         per_batch = 0
     else:
         raise ValueError(f"pos must be {want} or {(B, *want)}, got {tuple(pos.shape)}")
-    if freqs.dtype != torch.float64 or freqs.device != dev or freqs.dim() != 1 or not freqs.is_contiguous():
-        raise ValueError(f"freqs must be a contiguous fp64 [rot / 2] tensor on {dev}")
-    if out is not None:
-        if len(out) < len(xs):
+    if freqs.dtype != torch.float64 or freqs.get_device() != dev or freqs.dim() != 1 or not freqs.is_contiguous():
+        raise ValueError(f"freqs must be a contiguous fp64 [rot / 2] tensor on cuda:{dev}")
+    if out is None:
+        yq = torch.empty_like(q, memory_format=torch.contiguous_format)
+        yk = None if k is None else torch.empty_like(k, memory_format=torch.contiguous_format)
+    else:
+        if len(out) < (1 if k is None else 2):
             raise ValueError("out must hold a tensor for q and one for k")
-        for name, x, y in zip(("q", "k"), xs, out):
-            if y.shape != x.shape or y.dtype != dtype or y.device != dev or (x.numel() and y.stride(3) != 1):
-                raise ValueError(f"out for {name} must be {tuple(x.shape)} {dtype} on {dev}, channels contiguous")
-            if x.data_ptr() == y.data_ptr() and x.stride() != y.stride():
-                raise ValueError(f"out for {name} lies over it with other strides")
+        yq, yk = out[0], None if k is None else out[1]
+        _rotary_out(yq, q, "q", dev)
+        if k is not None:
+            _rotary_out(yk, k, "k", dev)
+    ys = yq.stride()
+    ts = _ROTARY_TENSOR.pack(q.data_ptr(), yq.data_ptr(), H, qs[0], qs[1], qs[2], ys[0], ys[1], ys[2])
+    if k is not None:
+        ys = yk.stride()
+        ts += _ROTARY_TENSOR.pack(k.data_ptr(), yk.data_ptr(), k.shape[2], ks[0], ks[1], ks[2], ys[0], ys[1], ys[2])
     sp = None if split is None else (ctypes.c_int32 * 3)(*[int(n) for n in split])
+    st = lib.jattn_rotary(ts, 1 if k is None else 2, code, B, S, d, parts, 2 * freqs.numel(), pos.data_ptr(), per_batch,
+                          sp, freqs.data_ptr(), _ROTARY_LAYOUT[layout], scale, inverse,
+                          torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise JattnError(st, "jattn_rotary")
+    return yq, yk
 
-    def call(st):
-        ys = tuple(torch.empty(x.shape, dtype=dtype, device=dev) for x in xs) if out is None else out
-        ts = b"".join([_ROTARY_TENSOR.pack(x.data_ptr(), y.data_ptr(), x.shape[2], *x.stride()[:3], *y.stride()[:3])
-                       for x, y in zip(xs, ys)])
-        _check(lib.jattn_rotary(ts, len(xs), _FLOAT_CODE[dtype], B, S, d, parts, 2 * freqs.numel(), pos.data_ptr(),
-                                per_batch, sp, freqs.data_ptr(), _ROTARY_LAYOUT[layout], scale, inverse, st),
-               "jattn_rotary")
-        return (ys[0], ys[1] if k is not None else None)
-    return _enqueue(dev, stream, (*xs, pos, freqs), call)
+
+def _rotary_out(y, x, name: str, dev: int):
+    if y.shape != x.shape or y.dtype != x.dtype or y.get_device() != dev or (x.numel() and y.stride(3) != 1):
+        raise ValueError(f"out for {name} must be {tuple(x.shape)} {x.dtype} on cuda:{dev}, channels contiguous")
+    if x.data_ptr() == y.data_ptr() and x.stride() != y.stride():
+        raise ValueError(f"out for {name} lies over it with other strides")
 
 
 def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtype=None, stream=None):
@@ -772,50 +793,61 @@ def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtyp
     given), or written to ``out``, which may be ``residual`` itself.  The last
     dimension must be contiguous and the leading ones one row range; rows
     whose stride and address are multiples of 16 bytes are the fast case."""
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a CUDA tensor")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: linear(x, w, bias, act, residual, out, out_dtype), dev, stream,
+                          (x, w, bias, residual, out))
     lib = load()
-    dev = _cuda_device(x, "x")
-    if x.dtype not in (torch.bfloat16, torch.float16):
+    code = _FLOAT_CODE.get(x.dtype)
+    if code is None or code == FP32:
         raise ValueError(f"x must be bf16 or fp16, got {x.dtype}")
-    if x.dim() < 1 or w.dim() != 2 or w.shape[1] != x.shape[-1]:
-        raise ValueError(f"x must be [..., K] and w [N, K], got {tuple(x.shape)} and {tuple(w.shape)}")
-    _on(w, "w", dev, (x.dtype,))
+    xs, ws = x.shape, w.shape
+    if len(xs) < 1 or len(ws) != 2 or ws[1] != xs[-1]:
+        raise ValueError(f"x must be [..., K] and w [N, K], got {tuple(xs)} and {tuple(ws)}")
+    _float_check(w, "w", dev, (x.dtype,))
     if act not in _ACT_CODE:
         raise ValueError(f"unknown activation {act!r}")
-    N, K = w.shape
+    N, K = ws
     if out is not None:
         out_dtype = out.dtype
     elif out_dtype is None:
         out_dtype = x.dtype
-    if out_dtype not in _FLOAT_CODE:
+    out_code = _FLOAT_CODE.get(out_dtype)
+    if out_code is None:
         raise ValueError(f"the output must be bf16, fp16 or fp32, got {out_dtype}")
-    shape = (*x.shape[:-1], N)
-    ldx, ldw = _rows(x, "x"), _rows(w, "w")
+    shape = (*xs[:-1], N)
+    ldx = K if x.is_contiguous() else _rows(x, "x")
+    ldw = K if w.is_contiguous() else _rows(w, "w")
+    bias_ptr, bias_code = None, 0
     if bias is not None:
-        _on(bias, "bias", dev, tuple(_FLOAT_CODE))
-        if tuple(bias.shape) != (N,) or (N > 1 and bias.stride(0) != 1):
+        _float_check(bias, "bias", dev, _FLOAT_CODE)
+        if bias.shape != (N,) or (N > 1 and bias.stride(0) != 1):
             raise ValueError(f"bias must be a contiguous [{N}], got {tuple(bias.shape)}")
-    ldr = N
+        bias_ptr, bias_code = bias.data_ptr(), _FLOAT_CODE[bias.dtype]
+    res_ptr, ldr = None, N
     if residual is not None:
-        _on(residual, "residual", dev, (out_dtype,))
-        if tuple(residual.shape) != shape:
+        _float_check(residual, "residual", dev, (out_dtype,))
+        if residual.shape != shape:
             raise ValueError(f"residual must be {shape}, got {tuple(residual.shape)}")
-        ldr = _rows(residual, "residual")
+        res_ptr = residual.data_ptr()
+        ldr = N if residual.is_contiguous() else _rows(residual, "residual")
     ldy = N
-    if out is not None:
-        _on(out, "out", dev, (out_dtype,))
-        if tuple(out.shape) != shape:
+    if out is None:
+        out = x.new_empty(shape, dtype=out_dtype)
+    else:
+        _float_check(out, "out", dev, (out_dtype,))
+        if out.shape != shape:
             raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
-        ldy = _rows(out, "out")
-    M = x.numel() // K if K else 0
-
-    def call(st):
-        y = torch.empty(shape, dtype=out_dtype, device=dev) if out is None else out
-        sh = _LINEAR_SHAPE.pack(M, N, K, ldx, ldw, ldy, ldr, _FLOAT_CODE[x.dtype], _FLOAT_CODE[out_dtype],
-                                0 if bias is None else _FLOAT_CODE[bias.dtype], _ACT_CODE[act])
-        _check(lib.jattn_linear(sh, x.data_ptr(), w.data_ptr(), None if bias is None else bias.data_ptr(),
-                                None if residual is None else residual.data_ptr(), y.data_ptr(), st), "jattn_linear")
-        return y
-    return _enqueue(dev, stream, (x, w, bias, residual, out), call)
+        ldy = N if out.is_contiguous() else _rows(out, "out")
+    st = lib.jattn_linear(_LINEAR_SHAPE.pack(x.numel() // K if K else 0, N, K, ldx, ldw, ldy, ldr, code, out_code,
+                                             bias_code, _ACT_CODE[act]),
+                          x.data_ptr(), w.data_ptr(), bias_ptr, res_ptr, out.data_ptr(),
+                          torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise JattnError(st, "jattn_linear")
+    return out
 
 
 def _rows(t, name: str) -> int:
@@ -849,51 +881,67 @@ def fwd_diff(q, k, v, lam, lambda_init: float, norm_w=None, eps: float = 1e-5, k
     norm_w and 1 - lambda_init.  kv_len: int32 [B], the valid keys of each
     batch entry.  key_mask: bool or uint8 [B, S_kv], nonzero where a key takes
     part.  Returns (o bf16 [B, S_q, H, d], lse fp32 [2, B, H, S_q] or None)."""
+    dev = q.get_device()
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return _elsewhere(lambda: fwd_diff(q, k, v, lam, lambda_init, norm_w, eps, kv_len, key_mask, o, lse, want_lse,
+                                           softmax_scale, workspace), dev, stream,
+                          (q, k, v, lam, norm_w, kv_len, key_mask, o, lse, workspace))
     lib = load()
-    dev = _cuda_device(q, "q")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"q must be [B, H, S_q, d] and k [B, H_kv, S_kv, d], got {tuple(q.shape)} and {tuple(k.shape)}")
     B, H, S_q, d = q.shape
-    H_kv, S_kv = k.shape[1], k.shape[2]
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"q must be bf16 or fp16, got {q.dtype}")
-    for name, t, n in (("q", q, q.shape), ("k", k, (B, H_kv, S_kv, d)), ("v", v, (B, H_kv, S_kv, d))):
-        if tuple(t.shape) != tuple(n) or t.dtype != q.dtype or t.device != dev:
-            raise ValueError(f"{name} must be {tuple(n)} {q.dtype} on {dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
-        if t.numel() and t.stride(3) != 1:
-            raise ValueError(f"{name}'s channels must be contiguous")
-    for name, t, dtypes, n in (("lam", lam, (torch.float32,), (4, H, d // 2)), ("norm_w", norm_w, (torch.float32,), (d,)),
-                               ("kv_len", kv_len, (torch.int32,), (B,)),
-                               ("key_mask", key_mask, (torch.bool, torch.uint8), (B, S_kv)),
-                               ("o", o, (torch.bfloat16,), (B, S_q, H, d)),
-                               ("lse", lse, (torch.float32,), (2, B, H, S_q))):
-        if t is None:
-            continue
-        _on(t, name, dev, dtypes)
-        if tuple(t.shape) != n or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {n}, got {tuple(t.shape)}")
-    sh = _DIFF_SHAPE.pack(B, H, H_kv, S_q, S_kv, d, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3])
-    need = lib.jattn_fwd_diff_workspace(sh, _FLOAT_CODE[q.dtype])
+    kshape = k.shape
+    H_kv, S_kv = kshape[1], kshape[2]
+    dtype = q.dtype
+    code = _FLOAT_CODE.get(dtype)
+    if code is None or code == FP32:
+        raise ValueError(f"q must be bf16 or fp16, got {dtype}")
+    if (kshape[0] != B or kshape[3] != d or v.shape != kshape or k.dtype != dtype or v.dtype != dtype or
+            k.get_device() != dev or v.get_device() != dev):
+        raise ValueError(f"k and v must be [{B}, H_kv, S_kv, {d}] {dtype} on cuda:{dev}, got {tuple(kshape)} {k.dtype} on "
+                         f"{k.device} and {tuple(v.shape)} {v.dtype} on {v.device}")
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if (qs[3] != 1 and q.numel()) or ((ks[3] != 1 or vs[3] != 1) and k.numel()):
+        raise ValueError("the channels of q, k and v must be contiguous")
+    _plain_check(lam, "lam", dev, _F32, (4, H, d // 2))
+    norm_ptr = len_ptr = mask_ptr = lse_ptr = ws_ptr = None
+    if norm_w is not None:
+        _plain_check(norm_w, "norm_w", dev, _F32, (d,))
+        norm_ptr = norm_w.data_ptr()
+    if kv_len is not None:
+        _plain_check(kv_len, "kv_len", dev, _I32, (B,))
+        len_ptr = kv_len.data_ptr()
+    if key_mask is not None:
+        _plain_check(key_mask, "key_mask", dev, _MASKS, (B, S_kv))
+        mask_ptr = key_mask.data_ptr()
+    if o is None:
+        o = q.new_empty((B, S_q, H, d), dtype=torch.bfloat16)
+    else:
+        _plain_check(o, "o", dev, _BF16, (B, S_q, H, d))
+    if lse is not None:
+        _plain_check(lse, "lse", dev, _F32, (2, B, H, S_q))
+    elif want_lse:
+        lse = q.new_empty((2, B, H, S_q), dtype=torch.float32)
+    if lse is not None:
+        lse_ptr = lse.data_ptr()
+    sh = _DIFF_SHAPE.pack(B, H, H_kv, S_q, S_kv, d, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
+    need = lib.jattn_fwd_diff_workspace(sh, code)
     if workspace is not None:
-        _on(workspace, "workspace", dev, (torch.uint8,))
+        _float_check(workspace, "workspace", dev, _BYTES)
         if not workspace.is_contiguous() or workspace.numel() < need:
             raise ValueError(f"workspace must hold at least {need} contiguous bytes, got {workspace.numel()}")
-
-    def call(st):
-        ws, oo, ll = workspace, o, lse
-        if ws is None and need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        if oo is None:
-            oo = torch.empty(B, S_q, H, d, dtype=torch.bfloat16, device=dev)
-        if ll is None and want_lse:
-            ll = torch.empty(2, B, H, S_q, dtype=torch.float32, device=dev)
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        _check(lib.jattn_fwd_diff(sh, _FLOAT_CODE[q.dtype], q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                  lam.data_ptr(), lambda_init, ptr(norm_w), eps, ptr(kv_len), ptr(key_mask), ptr(ws),
-                                  0 if ws is None else ws.numel(), oo.data_ptr(), ptr(ll), softmax_scale, st),
-               "jattn_fwd_diff")
-        return oo, ll
-    return _enqueue(dev, stream, (q, k, v, lam, norm_w, kv_len, key_mask, o, lse, workspace), call)
+    elif need:
+        workspace = q.new_empty(need, dtype=torch.uint8)
+    if workspace is not None:
+        ws_ptr = workspace.data_ptr()
+    st = lib.jattn_fwd_diff(sh, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), lam.data_ptr(), lambda_init, norm_ptr,
+                            eps, len_ptr, mask_ptr, ws_ptr, need, o.data_ptr(), lse_ptr, softmax_scale,
+                            torch._C._cuda_getCurrentRawStream(dev))
+    if st:
+        raise JattnError(st, "jattn_fwd_diff")
+    return o, lse
 
 
 def flops(B: int, H: int, S: int, d: int) -> int:
