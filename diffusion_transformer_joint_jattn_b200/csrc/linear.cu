@@ -61,32 +61,41 @@ __device__ __forceinline__ void store_from_f32(void* p, int64_t i, int dt, float
   else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// The activations, in fp32.  exp and the reciprocal are the hardware's
-// approximate ones (2^-21 relative or better, far under the 16-bit output's
-// rounding and at the level of the fp32 sum's own).
+// The activations, in fp32.  For 16-bit outputs exp and the reciprocal are the
+// hardware's approximate ones (2^-21 relative or better, far under the
+// output's rounding).
 __device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-template <int ACT>
+// For fp32 outputs: exp and the quotient correctly rounded to a few ulp.
+__device__ __forceinline__ float sigmoid_precise(float x) { return 1.f / (1.f + expf(-x)); }
+template <int ACT, bool PRECISE>
 __device__ __forceinline__ float activate_as(float x) {
+  auto sigmoid = [](float t) { return PRECISE ? sigmoid_precise(t) : sigmoid_f32(t); };
   if constexpr (ACT == JATTN_ACT_GELU) return 0.5f * x * (1.f + erff(x * 0.70710678118654752f));
   // 0.5 (1 + tanh u) = sigmoid(2 u)
-  if constexpr (ACT == JATTN_ACT_GELU_TANH) return x * sigmoid_f32(1.5957691216057308f * (x + 0.044715f * x * x * x));
-  if constexpr (ACT == JATTN_ACT_SILU) return x * sigmoid_f32(x);
+  if constexpr (ACT == JATTN_ACT_GELU_TANH) return x * sigmoid(1.5957691216057308f * (x + 0.044715f * x * x * x));
+  if constexpr (ACT == JATTN_ACT_SILU) return x * sigmoid(x);
   if constexpr (ACT == JATTN_ACT_RELU) return x < 0.f ? 0.f : x;     // keeps NaN
   return x;
 }
 template <int ACT, int W>
-__device__ __forceinline__ void activate_all(float (&v)[W]) {
+__device__ __forceinline__ void activate_all(float (&v)[W], bool precise) {
+  if (precise) {
 #pragma unroll
-  for (int i = 0; i < W; ++i) v[i] = activate_as<ACT>(v[i]);
+    for (int i = 0; i < W; ++i) v[i] = activate_as<ACT, true>(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W; ++i) v[i] = activate_as<ACT, false>(v[i]);
+  }
 }
 // One branch per array, not per element: the elements' chains interleave.
 template <int W>
-__device__ __forceinline__ void activate(float (&v)[W], int act) {
-  switch (act) {
-    case JATTN_ACT_GELU: activate_all<JATTN_ACT_GELU>(v); break;
-    case JATTN_ACT_GELU_TANH: activate_all<JATTN_ACT_GELU_TANH>(v); break;
-    case JATTN_ACT_SILU: activate_all<JATTN_ACT_SILU>(v); break;
-    case JATTN_ACT_RELU: activate_all<JATTN_ACT_RELU>(v); break;
+__device__ __forceinline__ void activate(float (&v)[W], const LinearParams& p) {
+  const bool precise = p.out_dtype == JATTN_FP32;
+  switch (p.act) {
+    case JATTN_ACT_GELU: activate_all<JATTN_ACT_GELU>(v, precise); break;
+    case JATTN_ACT_GELU_TANH: activate_all<JATTN_ACT_GELU_TANH>(v, precise); break;
+    case JATTN_ACT_SILU: activate_all<JATTN_ACT_SILU>(v, precise); break;
+    case JATTN_ACT_RELU: activate_all<JATTN_ACT_RELU>(v, precise); break;
     default: break;
   }
 }
@@ -101,9 +110,9 @@ __host__ __device__ inline int vector_bytes(const void* p, int64_t ld, int dt) {
 
 template <int WORDS>
 __device__ __forceinline__ void load_row(const uint32_t* src, uint32_t (&w)[WORDS], int vec) {
-  if (vec == 32) {
+  if (WORDS % 8 == 0 && vec == 32) {
 #pragma unroll
-    for (int i = 0; i < WORDS; i += 8)
+    for (int i = 0; i + 7 < WORDS; i += 8)
       asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                    : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3]), "=r"(w[i + 4]), "=r"(w[i + 5]),
                      "=r"(w[i + 6]), "=r"(w[i + 7])
@@ -119,9 +128,9 @@ __device__ __forceinline__ void load_row(const uint32_t* src, uint32_t (&w)[WORD
 }
 template <int WORDS>
 __device__ __forceinline__ void store_row(uint32_t* dst, const uint32_t (&w)[WORDS], int vec) {
-  if (vec == 32) {
+  if (WORDS % 8 == 0 && vec == 32) {
 #pragma unroll
-    for (int i = 0; i < WORDS; i += 8)
+    for (int i = 0; i + 7 < WORDS; i += 8)
       asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
                    ::"l"(dst + i), "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
                      "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
@@ -132,59 +141,60 @@ __device__ __forceinline__ void store_row(uint32_t* dst, const uint32_t (&w)[WOR
   }
 }
 
-// Columns [n, n + 32) of row m from the accumulator, bias already fp32 in
+// Columns [n, n + W) of row m from the accumulator, bias already fp32 in
 // shared memory (zeros past N or without a bias).
-__device__ __forceinline__ void finish_row(const LinearParams& p, float (&v)[32], const float* bias, int64_t m, int n) {
+template <int W>
+__device__ __forceinline__ void finish_row(const LinearParams& p, float (&v)[W], const float* bias, int64_t m, int n) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 4) {
+  for (int i = 0; i < W; i += 4) {
     const float4 b = *reinterpret_cast<const float4*>(bias + i);
     v[i] += b.x;
     v[i + 1] += b.y;
     v[i + 2] += b.z;
     v[i + 3] += b.w;
   }
-  activate(v, p.act);
+  activate(v, p);
   const bool f32 = p.out_dtype == JATTN_FP32, bf16 = p.out_dtype == JATTN_BF16;
-  const bool whole = n + 32 <= p.N;
+  const bool whole = n + W <= p.N;
   if (p.residual != nullptr) {
     const int64_t at = m * p.ldr + n;
     if (whole && p.vec_r != 0) {
       if (f32) {
-        uint32_t w[32];
+        uint32_t w[W];
         load_row(static_cast<const uint32_t*>(p.residual) + at, w, p.vec_r);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] += __uint_as_float(w[i]);
+        for (int i = 0; i < W; ++i) v[i] += __uint_as_float(w[i]);
       } else {
-        uint32_t w[16];
+        uint32_t w[W / 2];
         load_row(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.residual) + at), w, p.vec_r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < W / 2; ++i) {
           v[2 * i] += widen16(static_cast<uint16_t>(w[i]), bf16);
           v[2 * i + 1] += widen16(static_cast<uint16_t>(w[i] >> 16), bf16);
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < W; ++i)
         if (n + i < p.N) v[i] += load_as_f32(p.residual, at + i, p.out_dtype);
     }
   }
   const int64_t at = m * p.ldy + n;
   if (whole && p.vec_y != 0) {
     if (f32) {
-      uint32_t w[32];
+      uint32_t w[W];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+      for (int i = 0; i < W; ++i) w[i] = __float_as_uint(v[i]);
       store_row(static_cast<uint32_t*>(p.y) + at, w, p.vec_y);
     } else {
-      uint32_t w[16];
+      uint32_t w[W / 2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], bf16);
+      for (int i = 0; i < W / 2; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], bf16);
       store_row(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + at), w, p.vec_y);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
+    for (int i = 0; i < W; ++i)
       if (n + i < p.N) store_from_f32(p.y, at + i, p.out_dtype, v[i]);
   }
 }
@@ -208,6 +218,48 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// The MMA (one CTA's, or the pair's) and commit instructions by the lane with
+// `lead` set, the rest of the warp along: descriptors that the compiler knows
+// to be warp uniform live in uniform registers, where the instruction wants
+// them; in a branch of one lane each MMA took about 70 clocks to issue.
+template <int CTAS>
+__device__ __forceinline__ void mma_f16_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t acc) {
+  if constexpr (CTAS == 1)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n"
+      ::"r"(smem_u32(bar)), "r"(lead)
+      : "memory");
+}
+// Arrives at the same barrier of both CTAs.
+__device__ __forceinline__ void commit_pair_if(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}\n"
+      ::"r"(smem_u32(bar)), "r"(lead), "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 // Bounded wait of a whole warp (the tcgen05.ld that follows is collective).
@@ -284,32 +336,69 @@ struct TileCfg {
   static constexpr uint32_t TCOLS = BN < 32 ? 32u : static_cast<uint32_t>(BN);
 };
 
-// Stage rows [row0, row0 + rows) x [k0, k0 + 64) of a [n_rows][K] matrix in
-// the 128-byte swizzled layout, zeros outside; lane = two neighbouring k, a
-// warp's loads of 16 rows in flight before the first is stored.
-__device__ __forceinline__ void stage_plain(const uint16_t* g, int64_t ld, int64_t row0, int rows, int64_t n_rows, int k0,
-                                            int K, uint8_t* dst) {
-  constexpr int RB = 16;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k = k0 + 2 * lane;
-  const bool in0 = k < K, in1 = k + 1 < K;
-  const int ka = in0 ? k : 0, kb = in1 ? k + 1 : 0;
-  for (int r0 = warp; r0 < rows; r0 += 4 * RB) {
-    uint32_t lo[RB], hi[RB];
+// Operands whose rows TMA cannot address.  An element's 16 bytes of a swizzle
+// row lie in at most two aligned 16-byte pieces of memory: both are loaded
+// whole and shifted into place (element loads alone kept the load unit busy
+// four times as long as the MMAs take).
+struct Operand {
+  const uint16_t* g;
+  int64_t ld, rows;
+  int K;
+};
+// The aligned 16 bytes at `at` (elements; at a multiple of 8 from an aligned
+// address), or what of them lies inside the matrix's memory, element by
+// element.
+__device__ __forceinline__ uint4 piece(const uint16_t* at, const uint16_t* lo, const uint16_t* hi) {
+  if (at >= lo && at + 8 <= hi) return __ldg(reinterpret_cast<const uint4*>(at));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {                     // clamped, not skipped: no branch between the loads
-      const uint16_t* src = g + min(row0 + r0 + 4 * i, n_rows - 1) * ld;
-      lo[i] = __ldg(src + ka);
-      hi[i] = __ldg(src + kb);
-    }
+  for (int i = 0; i < 8; ++i)
+    if (at + i >= lo && at + i < hi) w[i >> 1] |= static_cast<uint32_t>(__ldg(at + i)) << (16 * (i & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Stage rows [row0, row0 + ROWS) x [k0, k0 + 64) in the 128-byte swizzled
+// layout, zeros outside the matrix.  8 threads per row, every load of the
+// stage in flight before the first is stored.
+template <int ROWS>
+__device__ __forceinline__ void stage_plain(const Operand& m, int64_t row0, int k0, uint8_t* dst) {
+  constexpr int ITEMS = (ROWS * 8 + kEpiThreads - 1) / kEpiThreads;
+  const int c = threadIdx.x & 7, k = k0 + c * 8;
+  const uint16_t* hi = m.g + (m.rows - 1) * m.ld + m.K;
+  uint4 x[ITEMS], y[ITEMS];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const int r = r0 + 4 * i;
-      const bool row_in = row0 + r < n_rows;
-      if (r < rows)
-        *reinterpret_cast<uint32_t*>(dst + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + ((lane & 3) << 2)) =
-            (row_in && in0 ? lo[i] : 0u) | (row_in && in1 ? hi[i] << 16 : 0u);
+  for (int i = 0; i < ITEMS; ++i) {
+    const int64_t row = min(row0 + (threadIdx.x >> 3) + i * (kEpiThreads / 8), m.rows - 1);
+    const uint16_t* src = m.g + row * m.ld + (k < m.K ? k : 0);
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) >> 1) & 7u;
+    x[i] = piece(src - off, m.g, hi);
+    y[i] = off != 0 ? piece(src - off + 8, m.g, hi) : make_uint4(0u, 0u, 0u, 0u);
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int r = (threadIdx.x >> 3) + i * (kEpiThreads / 8);
+    if (ROWS * 8 % kEpiThreads != 0 && r >= ROWS) break;
+    const int64_t row = min(row0 + r, m.rows - 1);
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(m.g + row * m.ld + (k < m.K ? k : 0)) >> 1) & 7u;
+    uint32_t w[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
+    if (off & 4u) {
+#pragma unroll
+      for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
     }
+    if (off & 2u) {
+#pragma unroll
+      for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+    }
+    if (off & 1u) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+    }
+    const int left = row0 + r < m.rows ? m.K - k : 0;    // elements inside the matrix
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (left <= 2 * j) w[j] = 0u;
+      else if (left == 2 * j + 1) w[j] &= 0xFFFFu;
+    }
+    *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -322,7 +411,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* sBias = reinterpret_cast<float*>(smem + C::DATA);
   TileBars* bar = reinterpret_cast<TileBars*>(smem + C::DATA + BN * 4);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // from one lane, so that the compiler sees the roles' branches as uniform
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   // tile (a, b) = rows a * 128 of A, rows b * BN of B; the cluster's CTAs
   // share a tile and take the K steps [kb, ke)
   const int split = p.splits, rank = split > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -332,7 +422,13 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   const int kb = static_cast<int>(static_cast<long long>(ksteps) * rank / split);
   const int ke = static_cast<int>(static_cast<long long>(ksteps) * (rank + 1) / split);
 
-  if (threadIdx.x == 0) {
+  auto load = [&](int k) {                               // K step k of the whole, into its stage
+    const int s = (k - kb) % C::ST;
+    mbar_arrive_expect_tx(&bar->full[s], C::STAGE);
+    tma_load_2d(&tmA, &bar->full[s], smem + s * C::STAGE, k * BK, ta * 128);
+    tma_load_2d(&tmB, &bar->full[s], smem + s * C::STAGE + 128 * BK * 2, k * BK, tb * BN);
+  };
+  if (threadIdx.x == 128) {
     for (int s = 0; s < C::ST; ++s) {
       mbar_init(&bar->full[s], TMA ? 1 : kEpiThreads);
       mbar_init(&bar->empty[s], 1);
@@ -340,12 +436,16 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     mbar_init(&bar->acc_full[0], 1);
     bar->abort = 0;
     fence_mbarrier_init();
+    // the first stages are free: their loads leave before the block meets
+    if (TMA)
+      for (int k = kb; k < min(ke, kb + C::ST); ++k) load(k);
   }
   if (warp == 5) {
     __syncwarp();
     tmem_alloc(&bar->tmem_base, C::TCOLS);
     tmem_relinquish();
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -355,13 +455,10 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   if (warp == 4) {
     if (TMA && lane == 0) {
       bool ok = true;
-      for (int k = kb; k < ke && ok; ++k) {
-        const int i = k - kb, s = i % C::ST;
-        ok = mbar_wait(&bar->empty[s], ((i / C::ST) & 1) ^ 1, ctl);
-        if (!ok) break;
-        mbar_arrive_expect_tx(&bar->full[s], C::STAGE);
-        tma_load_2d(&tmA, &bar->full[s], smem + s * C::STAGE, k * BK, ta * 128);
-        tma_load_2d(&tmB, &bar->full[s], smem + s * C::STAGE + 128 * BK * 2, k * BK, tb * BN);
+      for (int k = kb + C::ST; k < ke && ok; ++k) {
+        const int i = k - kb;
+        ok = mbar_wait(&bar->empty[i % C::ST], ((i / C::ST) & 1) ^ 1, ctl);
+        if (ok) load(k);
       }
       // the last stages' commits have arrived before the CTA may exit
       for (int i = ke - kb > C::ST ? ke - kb - C::ST : 0; i < ke - kb && ok; ++i)
@@ -369,21 +466,26 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       if (!ok) settle();
     }
   } else if (warp == 5) {
-    if (lane == 0) {
-      const uint32_t idesc = instr_desc(p.in_bf16, p.in_bf16, 0, 128, BN);
-      for (int k = kb; k < ke; ++k) {
-        const int i = k - kb, s = i % C::ST;
-        if (!mbar_wait(&bar->full[s], (i / C::ST) & 1, ctl)) break;
-        tc_fence_after();
-        const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + 128 * BK * 2;
+    // the whole warp walks, one lane issues (see mma_f16_if)
+    const uint32_t lead = elect_one() ? 1u : 0u;
+    const uint32_t idesc = instr_desc(p.in_bf16, p.in_bf16, 0, 128, BN);
+    const uint64_t ad0 = smem_desc(smem_u32(smem), 16, 1024, 2u), bd0 = ad0 + 128 * BK * 2 / 16;
+    int s = 0;
+    uint32_t par = 0;
+    for (int k = kb; k < ke; ++k) {
+      if (!warp_wait(&bar->full[s], par, ctl)) break;
+      tc_fence_after();
+      const uint32_t at = s * (C::STAGE / 16);
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk)
-          mma_f16_ss(tmem, smem_desc(a + kk * 32, 16, 1024, 2u), smem_desc(b + kk * 32, 16, 1024, 2u), idesc,
-                     i > 0 || kk > 0);
-        mma_commit(&bar->empty[s]);
+      for (int kk = 0; kk < BK / 16; ++kk)
+        mma_f16_if<1>(lead, tmem, ad0 + at + kk * 2, bd0 + at + kk * 2, idesc, k > kb || kk > 0);
+      commit_if(lead, &bar->empty[s]);
+      if (++s == C::ST) {
+        s = 0;
+        par ^= 1;
       }
-      mma_commit(&bar->acc_full[0]);
     }
+    commit_if(lead, &bar->acc_full[0]);
   } else {
     if (!TMA) {
       bool ok = true;
@@ -392,8 +494,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         ok = warp_wait(&bar->empty[s], ((i / C::ST) & 1) ^ 1, ctl);
         if (!ok) break;
         uint8_t* dst = smem + s * C::STAGE;
-        stage_plain(p.a, p.lda, static_cast<int64_t>(ta) * 128, 128, p.rows_a, k * BK, p.K, dst);
-        stage_plain(p.b, p.ldb, static_cast<int64_t>(tb) * BN, BN, p.rows_b, k * BK, p.K, dst + 128 * BK * 2);
+        stage_plain<128>({p.a, p.lda, p.rows_a, p.K}, static_cast<int64_t>(ta) * 128, k * BK, dst);
+        stage_plain<BN>({p.b, p.ldb, p.rows_b, p.K}, static_cast<int64_t>(tb) * BN, k * BK, dst + 128 * BK * 2);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         mbar_arrive(&bar->full[s]);
       }
@@ -446,7 +548,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         constexpr int W = sizeof(v) / sizeof(float);
 #pragma unroll
         for (int i = 0; i < W; ++i) v[i] += bias;
-        activate(v, p.act);
+        activate(v, p);
         const int64_t m = static_cast<int64_t>(tb) * BN + c;
         if (n >= p.N) return;
         if (p.residual != nullptr) {
@@ -487,36 +589,17 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     } else if constexpr (BN >= 32) {
       const int64_t m = static_cast<int64_t>(ta) * 128 + row;
       if (split > 1) {
-        // a share narrower than 32 columns is finished one element at a time
-        for (int c = c_lo; c < c_hi; c += 32) {
-          const int w = min(32, c_hi - c);
-          float v[32];
+        // a share of BN / split columns, 8 at a time
+        for (int c = c_lo; c < c_hi; c += 8) {
+          float v[8];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int i = 0; i < 8; ++i) v[i] = 0.f;
           for (int q = 0; q < split; ++q) {
             const uint32_t at = map_rank(red_addr + (c * 128 + row) * 4, q);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < w) v[i] += ld_cluster(at + i * 512);
+            for (int i = 0; i < 8; ++i) v[i] += ld_cluster(at + i * 512);
           }
-          if (m < p.M) {
-            if (w == 32) {
-              finish_row(p, v, sBias + c, m, tb * BN + c);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < w) v[i] += sBias[c + i];
-              activate(v, p.act);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int n = tb * BN + c + i;
-                if (i < w && n < p.N) {
-                  if (p.residual != nullptr) v[i] += load_as_f32(p.residual, m * p.ldr + n, p.out_dtype);
-                  store_from_f32(p.y, m * p.ldy + n, p.out_dtype, v[i]);
-                }
-              }
-            }
-          }
+          if (m < p.M && tb * BN + c < p.N) finish_row(p, v, sBias + c, m, tb * BN + c);
         }
       } else {
 #pragma unroll 1
@@ -562,7 +645,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* sBias = reinterpret_cast<float*>(smem + C::ST * C::STAGE);   // [4][256]
   TileBars* bar = reinterpret_cast<TileBars*>(smem + C::ST * C::STAGE + C::BIAS);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int tiles_n = (p.N + 255) / 256;
@@ -626,39 +709,34 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
       if (!ok) settle();
     }
   } else if (warp == 5) {
-    if (leader && lane == 0) {
+    if (leader) {
+      const uint32_t lead = elect_one() ? 1u : 0u;
       const uint32_t idesc = instr_desc(p.in_bf16, p.in_bf16, 0, 256, 256);
-      int it = 0, n = 0;
+      const uint64_t ad0 = smem_desc(smem_u32(smem), 16, 1024, 2u), bd0 = ad0 + 128 * BK * 2 / 16;
+      int s = 0, n = 0;
+      uint32_t par = 0;
       bool ok = true;
       for (long long t = pair; t < n_tiles && ok; t += n_pairs, ++n) {
         const int buf = n & 1;
-        ok = mbar_wait(&bar->acc_empty[buf], ((n >> 1) & 1) ^ 1, ctl);
+        ok = warp_wait(&bar->acc_empty[buf], ((n >> 1) & 1) ^ 1, ctl);
         if (!ok) break;
         tc_fence_after();
-        for (int k = 0; k < ksteps; ++k, ++it) {
-          const int s = it % C::ST;
-          ok = mbar_wait(&bar->full[s], (it / C::ST) & 1, ctl);
+        for (int k = 0; k < ksteps; ++k) {
+          ok = warp_wait(&bar->full[s], par, ctl);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + 128 * BK * 2;
+          const uint32_t at = s * (C::STAGE / 16);
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = smem_desc(a + kk * 32, 16, 1024, 2u), bd = smem_desc(b + kk * 32, 16, 1024, 2u);
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "setp.ne.b32 p, %4, 0;\n\t"
-                "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
-                ::"r"(tmem + buf * 256u), "l"(ad), "l"(bd), "r"(idesc), "r"(static_cast<uint32_t>(k > 0 || kk > 0))
-                : "memory");
+          for (int kk = 0; kk < BK / 16; ++kk)
+            mma_f16_if<2>(lead, tmem + buf * 256u, ad0 + at + kk * 2, bd0 + at + kk * 2, idesc, k > 0 || kk > 0);
+          commit_pair_if(lead, &bar->empty[s]);
+          if (++s == C::ST) {
+            s = 0;
+            par ^= 1;
           }
-          asm volatile(
-              "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-              ::"r"(smem_u32(&bar->empty[s])), "h"(static_cast<uint16_t>(3)) : "memory");
         }
         if (!ok) break;
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-            ::"r"(smem_u32(&bar->acc_full[buf])), "h"(static_cast<uint16_t>(3)) : "memory");
+        commit_pair_if(lead, &bar->acc_full[buf]);
       }
       if (!ok) settle();
     }
@@ -737,25 +815,34 @@ LinearPlan plan_linear(int M, int N, int K, bool tma) {
   LinearPlan pl{};
   const long long ksteps = (K + BK - 1) / BK;
   const long long pair_tiles = static_cast<long long>((M + 255) / 256) * ((N + 255) / 256);
-  if (tma && pair_tiles >= 74) {
+  // 256 x 256 tiles once they nearly fill the 74 pairs (1536 x 3000 x 1360, 72
+  // tiles: 17.6 us against 19.1; 1024 x 4096 x 1024, 64 tiles: 12.6 against
+  // 11.8)
+  if (tma && pair_tiles >= 68) {
     pl.pair = true;
     return pl;
   }
-  long long tiles;
-  if (M <= 64) {
-    pl.swap = true;
-    pl.bn = M <= 16 ? 16 : (M <= 32 ? 32 : 64);
-    tiles = static_cast<long long>((N + 127) / 128) * ((M + pl.bn - 1) / pl.bn);
-  } else {
-    pl.bn = 128;
-    tiles = static_cast<long long>((M + 127) / 128) * ((N + 127) / 128);
-    if (tiles < 148 || N <= 64) {
-      pl.bn = 64;
-      tiles = static_cast<long long>((M + 127) / 128) * ((N + 63) / 64);
-    }
-  }
   pl.splits = 1;
-  while (pl.splits < 8 && tiles * pl.splits * 2 <= 296 && ksteps / (pl.splits * 2) >= 4) pl.splits *= 2;
+  if (M <= 32) {
+    // W streams once: enough CTAs to draw on all of HBM, K steps enough to
+    // fill each one's pipeline (4 x 4096 x 4096: 11.1 us with 4 splits, 11.5
+    // with 8, 13.0 with 2; 4 x 16384 x 4096: 25.2 with 2, 27.7 with 1)
+    pl.swap = true;
+    pl.bn = M <= 16 ? 16 : 32;
+    const long long tiles = (N + 127) / 128;
+    while (pl.splits < 8 && (tiles * pl.splits < 100 ? ksteps / (pl.splits * 2) >= 4
+                                                     : tiles * pl.splits < 148 && ksteps / (pl.splits * 2) >= 32))
+      pl.splits *= 2;
+    return pl;
+  }
+  // 64 columns while two such CTAs fit on every SM, then 128; K is split only
+  // where the tiles leave SMs idle (1024 x 1024 x 1024, 128 tiles: 7.1 us whole,
+  // 9.7 in halves; 128 x 4096 x 4096, 64 tiles: 13.8 in quarters, 15.9 in
+  // halves)
+  const long long tiles = static_cast<long long>((M + 127) / 128) * ((N + 63) / 64);
+  pl.bn = tiles <= 296 ? 64 : 128;
+  if (tiles < 100)
+    while (pl.splits < 8 && tiles * pl.splits * 2 <= 296 && ksteps / (pl.splits * 2) >= 4) pl.splits *= 2;
   return pl;
 }
 
@@ -787,8 +874,7 @@ cudaError_t launch_linear(LinearParams p, const LinearPlan& pl, bool tma, const 
   const CUtensorMap& tb = pl.swap ? tx : tw;
   if (pl.swap) {
     if (pl.bn == 16) return tma ? launch_tile<16, true, true>(p, ta, tb, st) : launch_tile<16, true, false>(p, ta, tb, st);
-    if (pl.bn == 32) return tma ? launch_tile<32, true, true>(p, ta, tb, st) : launch_tile<32, true, false>(p, ta, tb, st);
-    return tma ? launch_tile<64, true, true>(p, ta, tb, st) : launch_tile<64, true, false>(p, ta, tb, st);
+    return tma ? launch_tile<32, true, true>(p, ta, tb, st) : launch_tile<32, true, false>(p, ta, tb, st);
   }
   if (pl.bn == 64) return tma ? launch_tile<64, false, true>(p, ta, tb, st) : launch_tile<64, false, false>(p, ta, tb, st);
   return tma ? launch_tile<128, false, true>(p, ta, tb, st) : launch_tile<128, false, false>(p, ta, tb, st);
