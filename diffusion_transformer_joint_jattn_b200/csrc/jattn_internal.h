@@ -175,25 +175,26 @@ struct LinearPlan {
 };
 struct LinearParams {
   int M, N, K;
-  const uint16_t *x, *w;
-  int64_t ldx, ldw, ldy, ldr;
+  int64_t ldy, ldr;
   const void* bias;             // [N] or null
   const void* residual;         // [M][N] of out_dtype, or null
   void* y;
   int in_bf16, out_dtype, bias_dtype, act;
   uint32_t* status;
   uint64_t timeout_ns;
-  // set by the launcher: the tile kernels' operands in their MMA roles
-  const uint16_t *a, *b;
-  int64_t lda, ldb, rows_a, rows_b;
+  // set by the launcher
   int tiles_a, tiles_b, splits;
   int vec_y, vec_r;             // bytes of the widest aligned access of y's and residual's rows, 0 = elements
 };
-LinearPlan plan_linear(int M, int N, int K, bool tma);
+LinearPlan plan_linear(int M, int N, int K);
 // tx, tw: 2-D maps with 64-element boxes of plan.pair ? 128 : (swap ? bn : 128) rows of x and
-// plan.pair ? 128 : (swap ? 128 : bn) rows of w; unused without tma.
-cudaError_t launch_linear(LinearParams p, const LinearPlan& plan, bool tma, const CUtensorMap& tx,
-                          const CUtensorMap& tw, cudaStream_t st);
+// plan.pair ? 128 : (swap ? 128 : bn) rows of w.
+cudaError_t launch_linear(LinearParams p, const LinearPlan& plan, const CUtensorMap& tx, const CUtensorMap& tw,
+                          cudaStream_t st);
+// Copies of up to two [rows][K] 16-bit operands (src null: none) into rows of K rounded up to 8 elements,
+// zeros behind K.
+cudaError_t launch_repack(const void* const src[2], void* const dst[2], const int64_t ld[2], const int64_t rows[2],
+                          int K, cudaStream_t st);
 
 // Differential attention.  n_groups row ranges per batch entry: H_kv ranges
 // of the packed rows (head, query) of the heads that share a K/V head, or H

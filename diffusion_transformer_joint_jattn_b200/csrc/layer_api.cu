@@ -100,6 +100,26 @@ DiffLayout diff_layout(const jattn_diff_shape* s, const DiffRanges& r, bool in_b
   return L;
 }
 
+int64_t padded(int64_t k) { return (k + 7) / 8 * 8; }
+
+// Which operands of the linear layer TMA cannot address (one row needs no
+// stride), and where their copies go in the workspace.
+struct LinearCopies {
+  bool x, w;
+  size_t w_at, total;
+};
+
+LinearCopies linear_copies(const jattn_linear_shape* s, const void* x, const void* w) {
+  LinearCopies c{};
+  if (s->M == 0 || s->N == 0) return c;
+  auto bytes = [&](int64_t rows) { return (static_cast<size_t>(rows) * padded(s->K) * 2 + 255) / 256 * 256; };
+  c.x = !aligned(x, 16) || (s->M > 1 && s->ldx % 8 != 0);
+  c.w = !aligned(w, 16) || (s->N > 1 && s->ldw % 8 != 0);
+  c.w_at = c.x ? bytes(s->M) : 0;
+  c.total = c.w_at + (c.w ? bytes(s->N) : 0);
+  return c;
+}
+
 }  // namespace
 
 namespace jattn {
@@ -176,8 +196,13 @@ jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors,
   return from_cuda(jattn::launch_rotary(p, dtype, layout == JATTN_ROTARY_HALF, static_cast<cudaStream_t>(stream)));
 }
 
+size_t jattn_linear_workspace(const jattn_linear_shape* s, const void* x, const void* w) {
+  if (s == nullptr || s->M < 0 || s->N < 0 || s->K < 1) return 0;
+  return linear_copies(s, x, w).total;
+}
+
 jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void* w, const void* bias,
-                          const void* residual, void* y, void* stream) {
+                          const void* residual, void* y, void* workspace, size_t workspace_bytes, void* stream) {
   if (s == nullptr || s->M < 0 || s->N < 0 || s->K < 1) return JATTN_ERR_INVALID_ARG;
   if (!is_16bit(s->in_dtype) || !is_float(s->out_dtype)) return JATTN_ERR_UNSUPPORTED;
   if (bias != nullptr && !is_float(s->bias_dtype)) return JATTN_ERR_UNSUPPORTED;
@@ -197,10 +222,6 @@ jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void
   p.M = s->M;
   p.N = s->N;
   p.K = s->K;
-  p.x = static_cast<const uint16_t*>(x);
-  p.w = static_cast<const uint16_t*>(w);
-  p.ldx = s->ldx;
-  p.ldw = s->ldw;
   p.ldy = s->ldy;
   p.ldr = s->ldr;
   p.bias = bias;
@@ -213,15 +234,27 @@ jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void
   p.timeout_ns = kTimeoutNs;
   p.status = jattn::device_status_ptr();
   if (p.status == nullptr) return JATTN_ERR_CUDA;
-  // one row needs no stride
-  const bool tma = aligned(x, 16) && aligned(w, 16) && (s->M == 1 || s->ldx % 8 == 0) && (s->N == 1 || s->ldw % 8 == 0);
-  const jattn::LinearPlan plan = jattn::plan_linear(s->M, s->N, s->K, tma);
-  CUtensorMap tx{}, tw{};
-  if (tma) {
-    const int bx = plan.pair ? 128 : (plan.swap ? plan.bn : 128), bw = plan.pair ? 128 : (plan.swap ? 128 : plan.bn);
-    if (!matrix_map(&tx, x, s->M, s->K, s->ldx, bx) || !matrix_map(&tw, w, s->N, s->K, s->ldw, bw)) return JATTN_ERR_CUDA;
+  // operands that TMA cannot address are copied into the workspace
+  const LinearCopies c = linear_copies(s, x, w);
+  if (c.total > 0) {
+    if (workspace == nullptr || workspace_bytes < c.total) return JATTN_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return JATTN_ERR_ALIGNMENT;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const void* src[2] = {c.x ? x : nullptr, c.w ? w : nullptr};
+    void* dst[2] = {ws, ws + c.w_at};
+    const int64_t ld[2] = {s->ldx, s->ldw}, rows[2] = {s->M, s->N};
+    if (jattn::launch_repack(src, dst, ld, rows, s->K, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return JATTN_ERR_CUDA;
+    if (c.x) x = dst[0];
+    if (c.w) w = dst[1];
   }
-  return from_cuda(jattn::launch_linear(p, plan, tma, tx, tw, static_cast<cudaStream_t>(stream)));
+  const jattn::LinearPlan plan = jattn::plan_linear(s->M, s->N, s->K);
+  CUtensorMap tx, tw;
+  const int bx = plan.pair ? 128 : (plan.swap ? plan.bn : 128), bw = plan.pair ? 128 : (plan.swap ? 128 : plan.bn);
+  if (!matrix_map(&tx, x, s->M, s->K, c.x ? padded(s->K) : s->ldx, bx) ||
+      !matrix_map(&tw, w, s->N, s->K, c.w ? padded(s->K) : s->ldw, bw))
+    return JATTN_ERR_CUDA;
+  return from_cuda(jattn::launch_linear(p, plan, tx, tw, static_cast<cudaStream_t>(stream)));
 }
 
 size_t jattn_fwd_diff_workspace(const jattn_diff_shape* shape, jattn_dtype in_dtype) {

@@ -13,8 +13,8 @@
 //          memory (in rank order: same bits every run, no workspace).  Few
 //          rows of x: the roles are swapped (W's rows are the MMA's 128 rows,
 //          x the BN), so the tile wastes no work on absent rows and W streams
-//          once.  Operands that TMA cannot address (row strides that are not
-//          multiples of 16 bytes) are staged by plain loads instead.
+//          once.
+// Operands that TMA cannot address are copied to rows that it can first.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -141,10 +141,20 @@ __device__ __forceinline__ void store_row(uint32_t* dst, const uint32_t (&w)[WOR
   }
 }
 
-// Columns [n, n + W) of row m from the accumulator, bias already fp32 in
-// shared memory (zeros past N or without a bias).
+// Floats of one warp's staging block: 32 rows of up to 32 columns, one word
+// apart so that neither its rows nor its columns share a bank.
+constexpr int kStageFloats = 32 * 33;
+
+// A whole warp: columns [n, n + W) of rows m0 + lane from the accumulator, bias
+// already fp32 in shared memory (zeros past N or without a bias).  Rows that
+// can be moved in 16 bytes are finished by their thread; others (odd row
+// strides, the last columns) go through `stage`, so that the lanes of an access
+// are neighbours in a row instead of 32 rows apart (1531 x 777 fp32: 60 -> XX us).
 template <int W>
-__device__ __forceinline__ void finish_row(const LinearParams& p, float (&v)[W], const float* bias, int64_t m, int n) {
+__device__ __forceinline__ void finish_rows(const LinearParams& p, float (&v)[W], const float* bias, int64_t m0, int n,
+                                            float* stage) {
+  const int lane = threadIdx.x & 31;
+  const int64_t m = m0 + lane;
 #pragma unroll
   for (int i = 0; i < W; i += 4) {
     const float4 b = *reinterpret_cast<const float4*>(bias + i);
@@ -155,47 +165,50 @@ __device__ __forceinline__ void finish_row(const LinearParams& p, float (&v)[W],
   }
   activate(v, p);
   const bool f32 = p.out_dtype == JATTN_FP32, bf16 = p.out_dtype == JATTN_BF16;
-  const bool whole = n + W <= p.N;
+  if (n + W > p.N || p.vec_y == 0 || (p.residual != nullptr && p.vec_r == 0)) {
+    __syncwarp();                                        // the block's last use is over
+#pragma unroll
+    for (int i = 0; i < W; ++i) stage[lane * (W + 1) + i] = v[i];
+    __syncwarp();
+    const int c = lane % W, n_at = n + c;
+#pragma unroll 4
+    for (int r = lane / W; r < 32; r += 32 / W) {
+      if (m0 + r >= p.M || n_at >= p.N) continue;
+      float x = stage[r * (W + 1) + c];
+      if (p.residual != nullptr) x += load_as_f32(p.residual, (m0 + r) * p.ldr + n_at, p.out_dtype);
+      store_from_f32(p.y, (m0 + r) * p.ldy + n_at, p.out_dtype, x);
+    }
+    return;
+  }
+  if (m >= p.M) return;
   if (p.residual != nullptr) {
     const int64_t at = m * p.ldr + n;
-    if (whole && p.vec_r != 0) {
-      if (f32) {
-        uint32_t w[W];
-        load_row(static_cast<const uint32_t*>(p.residual) + at, w, p.vec_r);
+    if (f32) {
+      uint32_t w[W];
+      load_row(static_cast<const uint32_t*>(p.residual) + at, w, p.vec_r);
 #pragma unroll
-        for (int i = 0; i < W; ++i) v[i] += __uint_as_float(w[i]);
-      } else {
-        uint32_t w[W / 2];
-        load_row(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.residual) + at), w, p.vec_r);
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-          v[2 * i] += widen16(static_cast<uint16_t>(w[i]), bf16);
-          v[2 * i + 1] += widen16(static_cast<uint16_t>(w[i] >> 16), bf16);
-        }
-      }
+      for (int i = 0; i < W; ++i) v[i] += __uint_as_float(w[i]);
     } else {
+      uint32_t w[W / 2];
+      load_row(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.residual) + at), w, p.vec_r);
 #pragma unroll
-      for (int i = 0; i < W; ++i)
-        if (n + i < p.N) v[i] += load_as_f32(p.residual, at + i, p.out_dtype);
+      for (int i = 0; i < W / 2; ++i) {
+        v[2 * i] += widen16(static_cast<uint16_t>(w[i]), bf16);
+        v[2 * i + 1] += widen16(static_cast<uint16_t>(w[i] >> 16), bf16);
+      }
     }
   }
   const int64_t at = m * p.ldy + n;
-  if (whole && p.vec_y != 0) {
-    if (f32) {
-      uint32_t w[W];
+  if (f32) {
+    uint32_t w[W];
 #pragma unroll
-      for (int i = 0; i < W; ++i) w[i] = __float_as_uint(v[i]);
-      store_row(static_cast<uint32_t*>(p.y) + at, w, p.vec_y);
-    } else {
-      uint32_t w[W / 2];
-#pragma unroll
-      for (int i = 0; i < W / 2; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], bf16);
-      store_row(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + at), w, p.vec_y);
-    }
+    for (int i = 0; i < W; ++i) w[i] = __float_as_uint(v[i]);
+    store_row(static_cast<uint32_t*>(p.y) + at, w, p.vec_y);
   } else {
+    uint32_t w[W / 2];
 #pragma unroll
-    for (int i = 0; i < W; ++i)
-      if (n + i < p.N) store_from_f32(p.y, at + i, p.out_dtype, v[i]);
+    for (int i = 0; i < W / 2; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], bf16);
+    store_row(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.y) + at), w, p.vec_y);
   }
 }
 
@@ -323,32 +336,34 @@ __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint64_
 
 // ---------------------------------------------------------------- one-CTA tiles
 
-// SWAP: the MMA's 128 rows are W's and its BN columns x's; TMA: operands by
-// TMA, else by plain loads of the epilogue warps.
-template <int BN, bool SWAP, bool TMA>
+// SWAP: the MMA's 128 rows are W's and its BN columns x's.
+template <int BN, bool SWAP>
 struct TileCfg {
   static constexpr int STAGE = (128 + BN) * BK * 2;
   static constexpr int ST = BN >= 128 ? 3 : (BN >= 64 ? 4 : 5);
   static constexpr int PIPE = ST * STAGE;
   static constexpr int RED = 128 * BN * 4;              // split K: this CTA's accumulator tile
-  static constexpr int DATA = PIPE > RED ? PIPE : RED;
+  static constexpr int DATA = PIPE;                     // behind RED, the epilogue's staging blocks
+  static_assert(SWAP ? PIPE >= RED : PIPE >= RED + 4 * 32 * 33 * 4, "room for the epilogue");
   static constexpr int SMEM = DATA + BN * 4 + 512 + 1024;
   static constexpr uint32_t TCOLS = BN < 32 ? 32u : static_cast<uint32_t>(BN);
 };
 
-// Operands whose rows TMA cannot address.  An element's 16 bytes of a swizzle
-// row lie in at most two aligned 16-byte pieces of memory: both are loaded
-// whole and shifted into place (element loads alone kept the load unit busy
-// four times as long as the MMAs take).
-struct Operand {
-  const uint16_t* g;
-  int64_t ld, rows;
-  int K;
+// Copies of operands whose rows TMA cannot address (row strides or addresses
+// that are not multiples of 16 bytes), rows of a multiple of 8 elements with
+// zeros behind K.  blockIdx.y = the operand.  A thread writes 8 elements; they
+// lie in at most two aligned 16-byte pieces, loaded whole and shifted into
+// place.  The copy costs one pass over the operand and the product then runs
+// at TMA's speed; staging such rows by plain loads inside the product took
+// 375 us for 9000 x 7000 x 501 and 58 us for 1531 x 777 x 1003, this XX and XX.
+struct RepackParams {
+  const uint16_t* src[2];
+  uint16_t* dst[2];
+  int64_t ld[2], rows[2];
+  int K, Kp;
 };
-// The aligned 16 bytes at `at` (elements; at a multiple of 8 from an aligned
-// address), or what of them lies inside the matrix's memory, element by
-// element.
-__device__ __forceinline__ uint4 piece(const uint16_t* at, const uint16_t* lo, const uint16_t* hi) {
+// The aligned 8 elements at `at`, or what of them lies in [lo, hi).
+__device__ __forceinline__ uint4 load_piece(const uint16_t* at, const uint16_t* lo, const uint16_t* hi) {
   if (at >= lo && at + 8 <= hi) return __ldg(reinterpret_cast<const uint4*>(at));
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -356,57 +371,41 @@ __device__ __forceinline__ uint4 piece(const uint16_t* at, const uint16_t* lo, c
     if (at + i >= lo && at + i < hi) w[i >> 1] |= static_cast<uint32_t>(__ldg(at + i)) << (16 * (i & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// Stage rows [row0, row0 + ROWS) x [k0, k0 + 64) in the 128-byte swizzled
-// layout, zeros outside the matrix.  8 threads per row, every load of the
-// stage in flight before the first is stored.
-template <int ROWS>
-__device__ __forceinline__ void stage_plain(const Operand& m, int64_t row0, int k0, uint8_t* dst) {
-  constexpr int ITEMS = (ROWS * 8 + kEpiThreads - 1) / kEpiThreads;
-  const int c = threadIdx.x & 7, k = k0 + c * 8;
-  const uint16_t* hi = m.g + (m.rows - 1) * m.ld + m.K;
-  uint4 x[ITEMS], y[ITEMS];
+__global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
+  const int op = blockIdx.y, chunks = p.Kp / 8;
+  const uint16_t* g = p.src[op];
+  if (g == nullptr) return;
+  const int64_t total = p.rows[op] * chunks;
+  const uint16_t* hi = g + (p.rows[op] - 1) * p.ld[op] + p.K;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = i / chunks;
+    const int k = static_cast<int>(i % chunks) * 8;
+    const uint16_t* at = g + row * p.ld[op] + k;
+    const uint32_t o = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) >> 1) & 7u;
+    const uint4 x = load_piece(at - o, g, hi);
+    const uint4 y = o != 0 ? load_piece(at - o + 8, g, hi) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int64_t row = min(row0 + (threadIdx.x >> 3) + i * (kEpiThreads / 8), m.rows - 1);
-    const uint16_t* src = m.g + row * m.ld + (k < m.K ? k : 0);
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src) >> 1) & 7u;
-    x[i] = piece(src - off, m.g, hi);
-    y[i] = off != 0 ? piece(src - off + 8, m.g, hi) : make_uint4(0u, 0u, 0u, 0u);
-  }
+    for (int j = 0; j < 6; ++j) w[j] = o & 4u ? w[j + 2] : w[j];
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int r = (threadIdx.x >> 3) + i * (kEpiThreads / 8);
-    if (ROWS * 8 % kEpiThreads != 0 && r >= ROWS) break;
-    const int64_t row = min(row0 + r, m.rows - 1);
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(m.g + row * m.ld + (k < m.K ? k : 0)) >> 1) & 7u;
-    uint32_t w[8] = {x[i].x, x[i].y, x[i].z, x[i].w, y[i].x, y[i].y, y[i].z, y[i].w};
-    if (off & 4u) {
+    for (int j = 0; j < 5; ++j) w[j] = o & 2u ? w[j + 1] : w[j];
+    const uint32_t sh = o & 1u ? 16u : 0u;
 #pragma unroll
-      for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
-    }
-    if (off & 2u) {
-#pragma unroll
-      for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
-    }
-    if (off & 1u) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
-    }
-    const int left = row0 + r < m.rows ? m.K - k : 0;    // elements inside the matrix
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], sh);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (left <= 2 * j) w[j] = 0u;
-      else if (left == 2 * j + 1) w[j] &= 0xFFFFu;
+      if (p.K - k <= 2 * j) w[j] = 0u;
+      else if (p.K - k == 2 * j + 1) w[j] &= 0xFFFFu;
     }
-    *reinterpret_cast<uint4*>(dst + r * 128 + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(p.dst[op] + row * p.Kp + k) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-template <int BN, bool SWAP, bool TMA>
+template <int BN, bool SWAP>
 __global__ void __launch_bounds__(kThreads, 2)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const LinearParams p) {
-  using C = TileCfg<BN, SWAP, TMA>;
+  using C = TileCfg<BN, SWAP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* sBias = reinterpret_cast<float*>(smem + C::DATA);
@@ -430,15 +429,14 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   };
   if (threadIdx.x == 128) {
     for (int s = 0; s < C::ST; ++s) {
-      mbar_init(&bar->full[s], TMA ? 1 : kEpiThreads);
+      mbar_init(&bar->full[s], 1);
       mbar_init(&bar->empty[s], 1);
     }
     mbar_init(&bar->acc_full[0], 1);
     bar->abort = 0;
     fence_mbarrier_init();
     // the first stages are free: their loads leave before the block meets
-    if (TMA)
-      for (int k = kb; k < min(ke, kb + C::ST); ++k) load(k);
+    for (int k = kb; k < min(ke, kb + C::ST); ++k) load(k);
   }
   if (warp == 5) {
     __syncwarp();
@@ -453,7 +451,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   const WaitCtl ctl{&bar->abort, p.status, p.timeout_ns};
 
   if (warp == 4) {
-    if (TMA && lane == 0) {
+    if (lane == 0) {
       bool ok = true;
       for (int k = kb + C::ST; k < ke && ok; ++k) {
         const int i = k - kb;
@@ -487,19 +485,6 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     }
     commit_if(lead, &bar->acc_full[0]);
   } else {
-    if (!TMA) {
-      bool ok = true;
-      for (int k = kb; k < ke && ok; ++k) {
-        const int i = k - kb, s = i % C::ST;
-        ok = warp_wait(&bar->empty[s], ((i / C::ST) & 1) ^ 1, ctl);
-        if (!ok) break;
-        uint8_t* dst = smem + s * C::STAGE;
-        stage_plain<128>({p.a, p.lda, p.rows_a, p.K}, static_cast<int64_t>(ta) * 128, k * BK, dst);
-        stage_plain<BN>({p.b, p.ldb, p.rows_b, p.K}, static_cast<int64_t>(tb) * BN, k * BK, dst + 128 * BK * 2);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        mbar_arrive(&bar->full[s]);
-      }
-    }
     if (!SWAP) {
       for (int i = threadIdx.x; i < BN; i += kEpiThreads) {
         const int n = tb * BN + i;
@@ -587,7 +572,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
         }
       }
     } else if constexpr (BN >= 32) {
-      const int64_t m = static_cast<int64_t>(ta) * 128 + row;
+      const int64_t m0 = static_cast<int64_t>(ta) * 128 + (warp & 3) * 32;
+      float* stage = reinterpret_cast<float*>(smem + C::RED) + (warp & 3) * kStageFloats;
       if (split > 1) {
         // a share of BN / split columns, 8 at a time
         for (int c = c_lo; c < c_hi; c += 8) {
@@ -599,7 +585,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += ld_cluster(at + i * 512);
           }
-          if (m < p.M && tb * BN + c < p.N) finish_row(p, v, sBias + c, m, tb * BN + c);
+          if (tb * BN + c < p.N) finish_rows(p, v, sBias + c, m0, tb * BN + c, stage);
         }
       } else {
 #pragma unroll 1
@@ -610,7 +596,7 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-          if (m < p.M && tb * BN + c < p.N) finish_row(p, v, sBias + c, m, tb * BN + c);
+          if (tb * BN + c < p.N) finish_rows(p, v, sBias + c, m0, tb * BN + c, stage);
         }
       }
     }
@@ -633,7 +619,8 @@ struct PairCfg {
   static constexpr int STAGE = (128 + 128) * BK * 2;     // per CTA: its rows of x, its rows of W
   static constexpr int ST = 6;
   static constexpr int BIAS = 4 * 256 * 4;               // each epilogue warp keeps its own copy
-  static constexpr int SMEM = ST * STAGE + BIAS + 512 + 1024;
+  static constexpr int OUT = 4 * 32 * 33 * 4;           // and a staging block
+  static constexpr int SMEM = ST * STAGE + BIAS + OUT + 512 + 1024;
 };
 constexpr int kGroupM = 8;                               // tiles of x a column of W tiles is used for in a row
 
@@ -644,7 +631,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* sBias = reinterpret_cast<float*>(smem + C::ST * C::STAGE);   // [4][256]
-  TileBars* bar = reinterpret_cast<TileBars*>(smem + C::ST * C::STAGE + C::BIAS);
+  TileBars* bar = reinterpret_cast<TileBars*>(smem + C::ST * C::STAGE + C::BIAS + C::OUT);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -742,6 +729,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
     }
   } else {
     const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    float* stage = reinterpret_cast<float*>(smem + C::ST * C::STAGE + C::BIAS) + warp * kStageFloats;
     int n = 0;
     for (long long t = pair; t < n_tiles; t += n_pairs, ++n) {
       int tm, tn;
@@ -758,7 +746,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
       if (!warp_wait(&bar->acc_full[buf], (n >> 1) & 1, ctl)) break;
       __syncwarp();
       tc_fence_after();
-      const int64_t m = static_cast<int64_t>(tm) * 256 + rank * 128 + warp * 32 + lane;
+      const int64_t m0 = static_cast<int64_t>(tm) * 256 + rank * 128 + warp * 32;
 #pragma unroll 1
       for (int c = 0; c < 256; c += 32) {
         uint32_t r[32];
@@ -767,7 +755,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-        if (m < p.M && tn * 256 + c < p.N) finish_row(p, v, bias + c, m, tn * 256 + c);
+        if (tn * 256 + c < p.N) finish_rows(p, v, bias + c, m0, tn * 256 + c, stage);
       }
       tc_fence_before();
       __syncwarp();
@@ -785,10 +773,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   }
 }
 
-template <int BN, bool SWAP, bool TMA>
+template <int BN, bool SWAP>
 cudaError_t launch_tile(const LinearParams& p, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st) {
-  using C = TileCfg<BN, SWAP, TMA>;
-  auto kern = linear_tile_kernel<BN, SWAP, TMA>;
+  using C = TileCfg<BN, SWAP>;
+  auto kern = linear_tile_kernel<BN, SWAP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.tiles_a) * p.tiles_b * p.splits;
@@ -811,14 +799,14 @@ cudaError_t launch_tile(const LinearParams& p, const CUtensorMap& ta, const CUte
 }  // namespace
 
 // The kernel, tile and split of one problem: pure host arithmetic.
-LinearPlan plan_linear(int M, int N, int K, bool tma) {
+LinearPlan plan_linear(int M, int N, int K) {
   LinearPlan pl{};
   const long long ksteps = (K + BK - 1) / BK;
   const long long pair_tiles = static_cast<long long>((M + 255) / 256) * ((N + 255) / 256);
   // 256 x 256 tiles once they nearly fill the 74 pairs (1536 x 3000 x 1360, 72
   // tiles: 17.6 us against 19.1; 1024 x 4096 x 1024, 64 tiles: 12.6 against
   // 11.8)
-  if (tma && pair_tiles >= 68) {
+  if (pair_tiles >= 68) {
     pl.pair = true;
     return pl;
   }
@@ -846,7 +834,25 @@ LinearPlan plan_linear(int M, int N, int K, bool tma) {
   return pl;
 }
 
-cudaError_t launch_linear(LinearParams p, const LinearPlan& pl, bool tma, const CUtensorMap& tx, const CUtensorMap& tw,
+cudaError_t launch_repack(const void* const src[2], void* const dst[2], const int64_t ld[2], const int64_t rows[2],
+                          int K, cudaStream_t st) {
+  RepackParams p{};
+  p.K = K;
+  p.Kp = static_cast<int>((static_cast<int64_t>(K) + 7) / 8 * 8);
+  int64_t most = 0;
+  for (int i = 0; i < 2; ++i) {
+    p.src[i] = static_cast<const uint16_t*>(src[i]);
+    p.dst[i] = static_cast<uint16_t*>(dst[i]);
+    p.ld[i] = ld[i];
+    p.rows[i] = rows[i];
+    if (src[i] != nullptr && rows[i] > most) most = rows[i];
+  }
+  const int64_t blocks = (most * (p.Kp / 8) + 255) / 256, cap = 16ll * device_sm_count();
+  repack_kernel<<<dim3(static_cast<unsigned>(blocks < cap ? blocks : cap), 2), 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_linear(LinearParams p, const LinearPlan& pl, const CUtensorMap& tx, const CUtensorMap& tw,
                           cudaStream_t st) {
   p.vec_y = vector_bytes(p.y, p.ldy, p.out_dtype);
   p.vec_r = p.residual != nullptr ? vector_bytes(p.residual, p.ldr, p.out_dtype) : 0;
@@ -864,20 +870,10 @@ cudaError_t launch_linear(LinearParams p, const LinearPlan& pl, bool tma, const 
   const int rows_a = pl.swap ? p.N : p.M, rows_b = pl.swap ? p.M : p.N;
   p.tiles_a = (rows_a + 127) / 128;
   p.tiles_b = (rows_b + pl.bn - 1) / pl.bn;
-  p.rows_a = rows_a;
-  p.rows_b = rows_b;
-  p.a = pl.swap ? p.w : p.x;
-  p.b = pl.swap ? p.x : p.w;
-  p.lda = pl.swap ? p.ldw : p.ldx;
-  p.ldb = pl.swap ? p.ldx : p.ldw;
   const CUtensorMap& ta = pl.swap ? tw : tx;
   const CUtensorMap& tb = pl.swap ? tx : tw;
-  if (pl.swap) {
-    if (pl.bn == 16) return tma ? launch_tile<16, true, true>(p, ta, tb, st) : launch_tile<16, true, false>(p, ta, tb, st);
-    return tma ? launch_tile<32, true, true>(p, ta, tb, st) : launch_tile<32, true, false>(p, ta, tb, st);
-  }
-  if (pl.bn == 64) return tma ? launch_tile<64, false, true>(p, ta, tb, st) : launch_tile<64, false, false>(p, ta, tb, st);
-  return tma ? launch_tile<128, false, true>(p, ta, tb, st) : launch_tile<128, false, false>(p, ta, tb, st);
+  if (pl.swap) return pl.bn == 16 ? launch_tile<16, true>(p, ta, tb, st) : launch_tile<32, true>(p, ta, tb, st);
+  return pl.bn == 64 ? launch_tile<64, false>(p, ta, tb, st) : launch_tile<128, false>(p, ta, tb, st);
 }
 
 }  // namespace jattn

@@ -45,7 +45,7 @@ SYMBOLS = ("jattn_rope_qkv", "jattn_rope_qkv_norm", "jattn_quant_fp8", "jattn_fw
            "jattn_joint_attention_host", "jattn_joint_attention_host_workspace", "jattn_fwd_bf16", "jattn_fwd_fp8",
            "jattn_rope_qkv_hp", "jattn_rope_qkv_hp_workspace", "jattn_fwd_bf16_hp",
            "jattn_fwd_block_sparse", "jattn_fwd_block_sparse_workspace",
-           "jattn_rotary", "jattn_linear", "jattn_fwd_diff", "jattn_fwd_diff_workspace",
+           "jattn_rotary", "jattn_linear", "jattn_linear_workspace", "jattn_fwd_diff", "jattn_fwd_diff_workspace",
            "jattn_device_status", "jattn_last_device_status", "jattn_selftest_wait_timeout", "jattn_status_string",
            "jattn_version")
 
@@ -104,7 +104,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jattn_fwd_fp8.argtypes = [sp, vp, vp, vp, vp, vp, vp, f32, vp]
     lib.jattn_rotary.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, vp, ctypes.c_int64,
                                  ctypes.POINTER(i32), vp, i32, f32, i32, vp]
-    lib.jattn_linear.argtypes = [vp, vp, vp, vp, vp, vp, vp]
+    lib.jattn_linear.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.jattn_linear_workspace.argtypes = [vp, vp, vp]
     lib.jattn_fwd_diff.argtypes = [vp, i32, vp, vp, vp, vp, f32, vp, f32, vp, vp, vp,
                                    ctypes.c_size_t, vp, vp, f32, vp]
     lib.jattn_fwd_diff_workspace.argtypes = [vp, i32]
@@ -121,6 +122,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.jattn_rope_qkv_hp_workspace.restype = ctypes.c_size_t
     lib.jattn_fwd_block_sparse_workspace.restype = ctypes.c_size_t
     lib.jattn_joint_attention_host_workspace.restype = ctypes.c_size_t
+    lib.jattn_linear_workspace.restype = ctypes.c_size_t
     lib.jattn_fwd_diff_workspace.restype = ctypes.c_size_t
     _lib = lib
     return lib
@@ -650,7 +652,13 @@ def _plain_check(t, name: str, dev: int, dtypes, shape):
                          f"cuda:{dev}, got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
-_F32, _F64, _I32, _BYTES, _BF16 = (torch.float32,), (torch.float64,), (torch.int32,), (torch.uint8,), (torch.bfloat16,)
+def _workspace_check(t, dev: int, need: int):
+    _float_check(t, "workspace", dev, (torch.uint8,))
+    if not t.is_contiguous() or t.numel() < need:
+        raise ValueError(f"workspace must hold at least {need} contiguous bytes, got {t.numel()}")
+
+
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _MASKS = (torch.bool, torch.uint8)
 
 
@@ -784,21 +792,23 @@ def _rotary_out(y, x, name: str, dev: int):
         raise ValueError(f"out for {name} lies over it with other strides")
 
 
-def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtype=None, stream=None):
+def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtype=None, workspace=None,
+           stream=None):
     """act(x w^T + bias) + residual (jattn_linear): x [..., K], w [N, K] of one
     16-bit type, bias [N] (any float type), residual [..., N] of the output's
     type; sums and epilogue in fp32.  act: none, gelu, gelu_tanh, silu, relu.
 
     Output [..., N] of ``out_dtype`` (bf16, fp16 or fp32; x's type unless
     given), or written to ``out``, which may be ``residual`` itself.  The last
-    dimension must be contiguous and the leading ones one row range; rows
-    whose stride and address are multiples of 16 bytes are the fast case."""
+    dimension must be contiguous and the leading ones one row range.  An x or w
+    whose address or row stride is not a multiple of 16 bytes is copied first,
+    into ``workspace`` (a uint8 CUDA tensor, allocated here when None)."""
     dev = x.get_device()
     if dev < 0:
         raise ValueError("x must be a CUDA tensor")
     if stream is not None or dev != torch._C._cuda_getDevice():
-        return _elsewhere(lambda: linear(x, w, bias, act, residual, out, out_dtype), dev, stream,
-                          (x, w, bias, residual, out))
+        return _elsewhere(lambda: linear(x, w, bias, act, residual, out, out_dtype, workspace), dev, stream,
+                          (x, w, bias, residual, out, workspace))
     lib = load()
     code = _FLOAT_CODE.get(x.dtype)
     if code is None or code == FP32:
@@ -841,9 +851,17 @@ def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtyp
         if out.shape != shape:
             raise ValueError(f"out must be {shape}, got {tuple(out.shape)}")
         ldy = N if out.is_contiguous() else _rows(out, "out")
-    st = lib.jattn_linear(_LINEAR_SHAPE.pack(x.numel() // K if K else 0, N, K, ldx, ldw, ldy, ldr, code, out_code,
-                                             bias_code, _ACT_CODE[act]),
-                          x.data_ptr(), w.data_ptr(), bias_ptr, res_ptr, out.data_ptr(),
+    sh = _LINEAR_SHAPE.pack(x.numel() // K if K else 0, N, K, ldx, ldw, ldy, ldr, code, out_code, bias_code,
+                            _ACT_CODE[act])
+    px, pw, ws_ptr = x.data_ptr(), w.data_ptr(), None
+    need = lib.jattn_linear_workspace(sh, px, pw) if (px | pw | 2 * ldx | 2 * ldw) & 15 else 0
+    if need:
+        if workspace is None:
+            workspace = x.new_empty(need, dtype=torch.uint8)
+        else:
+            _workspace_check(workspace, dev, need)
+        ws_ptr = workspace.data_ptr()
+    st = lib.jattn_linear(sh, px, pw, bias_ptr, res_ptr, out.data_ptr(), ws_ptr, need,
                           torch._C._cuda_getCurrentRawStream(dev))
     if st:
         raise JattnError(st, "jattn_linear")
@@ -929,9 +947,7 @@ def fwd_diff(q, k, v, lam, lambda_init: float, norm_w=None, eps: float = 1e-5, k
     sh = _DIFF_SHAPE.pack(B, H, H_kv, S_q, S_kv, d, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
     need = lib.jattn_fwd_diff_workspace(sh, code)
     if workspace is not None:
-        _float_check(workspace, "workspace", dev, _BYTES)
-        if not workspace.is_contiguous() or workspace.numel() < need:
-            raise ValueError(f"workspace must hold at least {need} contiguous bytes, got {workspace.numel()}")
+        _workspace_check(workspace, dev, need)
     elif need:
         workspace = q.new_empty(need, dtype=torch.uint8)
     if workspace is not None:

@@ -431,15 +431,19 @@ typedef struct {
  * epilogue in fp32, one rounding.
  *   x [M][K], w [N][K] : in_dtype;  bias [N] or NULL;  residual [M][N] or
  *   NULL (may be y itself, with ldr == ldy; y overlaps nothing else).
- * Any sizes and strides; x and w whose pointers and row strides are multiples
- * of 16 bytes are moved by TMA, others by element loads (slower).  No
- * workspace; the same call gives the same bits every time.
+ * Any sizes and strides.  An x or w whose address or row stride is not a
+ * multiple of 16 bytes is first copied into the workspace: device scratch of
+ * at least jattn_linear_workspace(shape, x, w) bytes, 256-byte aligned (NULL
+ * where that is 0).  Calls that may overlap on the GPU need one each.  The
+ * same call gives the same bits every time.
  * Errors: JATTN_ERR_INVALID_ARG, JATTN_ERR_UNSUPPORTED (types, act),
  * JATTN_ERR_ALIGNMENT (a pointer not aligned to its element).  M or N of 0 is
  * no work and JATTN_OK.
  */
+/* 0: none needed, or invalid arguments */
+size_t jattn_linear_workspace(const jattn_linear_shape* shape, const void* x, const void* w);
 jattn_status jattn_linear(const jattn_linear_shape* shape, const void* x, const void* w, const void* bias,
-                          const void* residual, void* y, void* stream);
+                          const void* residual, void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Differential attention's shape.  Strides in elements over (batch entry,
  * head, token), multiples of 8; channels contiguous.  d in {64, 128};
