@@ -610,48 +610,52 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         while (globaltimer_ns() - t < 1000000ull) {
         }
       }
-    } else if (warp == kMaskWarp && KIND != kBf16WideV && (p.key_mask != nullptr || p.kv_len != nullptr)) {
-      int nv = 0;
-      Segment s;
-      bool ok = true;
-      for (Walk walk(p, share); ok && walk.next(p, share, s);) {
-        const bool fix = fixes(s);
-        const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(s.b) * p.S_kv : nullptr;
-        for (int j = 0; j < s.n_kv; ++j, ++nv) {
-          const int vs = nv % C::VS, key0 = (s.t0 + j) * BN;
-          if (!fix) {
-            // keep v_ready's phase with the stage's
-            ok = warp_wait(&bar->v_full[vs], (nv / C::VS) & 1, ctl);
-            if (!ok) break;
-            if (lane == 0) mbar_arrive(&bar->v_ready[vs]);
-            continue;
-          }
-          bool drop[4];                                 // keys key0 + 32 w + lane
+    } else if (warp == kMaskWarp) {
+      if constexpr (KIND != kBf16WideV) {
+        if (p.key_mask != nullptr || p.kv_len != nullptr) {
+          int nv = 0;
+          Segment s;
+          bool ok = true;
+          for (Walk walk(p, share); ok && walk.next(p, share, s);) {
+            const bool fix = fixes(s);
+            const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(s.b) * p.S_kv : nullptr;
+            for (int j = 0; j < s.n_kv; ++j, ++nv) {
+              const int vs = nv % C::VS, key0 = (s.t0 + j) * BN;
+              if (!fix) {
+                // keep v_ready's phase with the stage's
+                ok = warp_wait(&bar->v_full[vs], (nv / C::VS) & 1, ctl);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&bar->v_ready[vs]);
+                continue;
+              }
+              bool drop[4];                                 // keys key0 + 32 w + lane
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int key = key0 + 32 * w + lane;
-            drop[w] = key < p.S_kv && (key >= s.len || (mask != nullptr && __ldg(mask + key) == 0));
-          }
-          ok = warp_wait(&bar->v_full[vs], (nv / C::VS) & 1, ctl);
-          if (!ok) break;
-          uint8_t* tile = sV + vs * C::TB;
-          bool wrote = false;
+              for (int w = 0; w < 4; ++w) {
+                const int key = key0 + 32 * w + lane;
+                drop[w] = key < p.S_kv && (key >= s.len || (mask != nullptr && __ldg(mask + key) == 0));
+              }
+              ok = warp_wait(&bar->v_full[vs], (nv / C::VS) & 1, ctl);
+              if (!ok) break;
+              uint8_t* tile = sV + vs * C::TB;
+              bool wrote = false;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t todo = __ballot_sync(0xffffffffu, drop[w]);
-            wrote = wrote || todo != 0;
-            // a row is 128 bytes of each box, wherever the swizzle put its pieces
-            while (todo != 0) {
-              const int r = 32 * w + __ffs(todo) - 1;
-              todo &= todo - 1;
+              for (int w = 0; w < 4; ++w) {
+                uint32_t todo = __ballot_sync(0xffffffffu, drop[w]);
+                wrote = wrote || todo != 0;
+                // a row is 128 bytes of each box, wherever the swizzle put its pieces
+                while (todo != 0) {
+                  const int r = 32 * w + __ffs(todo) - 1;
+                  todo &= todo - 1;
 #pragma unroll
-              for (int x = 0; x < C::NBOX; ++x)
-                *reinterpret_cast<uint32_t*>(tile + x * C::BOXB + r * 128 + lane * 4) = 0u;
+                  for (int x = 0; x < C::NBOX; ++x)
+                    *reinterpret_cast<uint32_t*>(tile + x * C::BOXB + r * 128 + lane * 4) = 0u;
+                }
+              }
+              if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar->v_ready[vs]);
             }
           }
-          if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->v_ready[vs]);
         }
       }
     }
@@ -673,6 +677,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const bool warp_live = s.rt * BM + (warp & 3) * 32 < p.R;
       const int head = s.gi * p.hpg + (live ? r / p.S_q : 0), s_q = live ? r % p.S_q : 0;
       const int n = s.n_half, key0 = s.t0 * BN;
+      // needed at the end; read while the first tiles are on their way
+      const float lam = s.whole && live ? lambda_of(p, head, DM) : 0.f;
       float m_run = -INFINITY, l_run = 0.f;
       uint8_t mb[2] = {1, 1};
       auto load_mask = [&](int i) {
@@ -811,7 +817,6 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tc_fence_before();                              // before the next segment's P.V overwrites O_t
         continue;
       }
-      const float lam = live ? lambda_of(p, head, DM) : 0.f;
       sL[t * BM + row] = inv;
       tc_fence_before();
       mbar_arrive(&bar->exchange[0]);
@@ -889,6 +894,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Merge of the items that several CTAs shared, one warp per query row: each
@@ -901,6 +907,7 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
   const int cta = blockIdx.x + 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long total = shared_prefix(p, p.B);
   const long long g = share_start(total, cta, ctas);
   if (g >= total) return;
@@ -1002,8 +1009,17 @@ cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorM
   kern<<<p.ctas, kThreads, C::SMEM, st>>>(tq, tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess || !p.merge) return e;
   const dim3 grid(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>(((p.R < BM ? p.R : BM) + 3) / 4));
-  diff_merge_kernel<D><<<grid, 128, 0, st>>>(p, p.ctas);
-  return cudaGetLastError();
+  // launched while the walk runs (it waits for its end before it reads)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, diff_merge_kernel<D>, p, p.ctas);
 }
 
 template <int D>

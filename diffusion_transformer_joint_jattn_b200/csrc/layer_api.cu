@@ -60,7 +60,7 @@ jattn_status diff_ranges(const jattn_diff_shape* s, DiffRanges* r) {
   const int64_t size[3][3] = {{s->B, s->H, s->S_q}, {s->B, s->H_kv, s->S_kv}, {s->B, s->H_kv, s->S_kv}};
   const int64_t* stride[3] = {s->q_stride, s->k_stride, s->v_stride};
   for (int t = 0; t < 3; ++t)
-    for (int i = 0; i < 3; ++i)
+    for (int i = 0; i < 3 && size[t][0] * size[t][2] > 0; ++i)     // no elements: no strides
       if (size[t][i] > 1 && (stride[t][i] < s->d || stride[t][i] % 8 != 0 || stride[t][i] >= (int64_t{1} << 38)))
         return JATTN_ERR_INVALID_ARG;
   const int G = s->H / s->H_kv;
@@ -218,6 +218,10 @@ jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void
   if (!aligned(x, 2) || !aligned(w, 2) || !aligned(y, ob)) return JATTN_ERR_ALIGNMENT;
   if (residual != nullptr && !aligned(residual, ob)) return JATTN_ERR_ALIGNMENT;
   if (bias != nullptr && !aligned(bias, elem_bytes(s->bias_dtype))) return JATTN_ERR_ALIGNMENT;
+  // operands that TMA cannot address are copied into the workspace
+  const LinearCopies c = linear_copies(s, x, w);
+  if (c.total > 0 && (workspace == nullptr || workspace_bytes < c.total)) return JATTN_ERR_INVALID_ARG;
+  if (c.total > 0 && !aligned(workspace, 256)) return JATTN_ERR_ALIGNMENT;
   jattn::LinearParams p{};
   p.M = s->M;
   p.N = s->N;
@@ -234,11 +238,7 @@ jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void
   p.timeout_ns = kTimeoutNs;
   p.status = jattn::device_status_ptr();
   if (p.status == nullptr) return JATTN_ERR_CUDA;
-  // operands that TMA cannot address are copied into the workspace
-  const LinearCopies c = linear_copies(s, x, w);
   if (c.total > 0) {
-    if (workspace == nullptr || workspace_bytes < c.total) return JATTN_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256)) return JATTN_ERR_ALIGNMENT;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const void* src[2] = {c.x ? x : nullptr, c.w ? w : nullptr};
     void* dst[2] = {ws, ws + c.w_at};

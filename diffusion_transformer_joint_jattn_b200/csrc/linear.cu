@@ -65,8 +65,15 @@ __device__ __forceinline__ void store_from_f32(void* p, int64_t i, int dt, float
 // hardware's approximate ones (2^-21 relative or better, far under the
 // output's rounding).
 __device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-// For fp32 outputs: exp and the quotient correctly rounded to a few ulp.
-__device__ __forceinline__ float sigmoid_precise(float x) { return 1.f / (1.f + expf(-x)); }
+// For fp32 outputs: exp to 2 ulp, the reciprocal with one Newton step (without
+// the branches of a division, which kept the elements of a row from
+// interleaving: 8 us on a 128 x 128 tile).  Below -87, where x sigmoid(x) is
+// under 2^-118, exp stays at e^87 so that the reciprocal stays normal.
+__device__ __forceinline__ float sigmoid_precise(float x) {
+  const float d = 1.f + expf(fminf(-x, 87.f));
+  const float r = __fdividef(1.f, d);
+  return fmaf(r, fmaf(-d, r, 1.f), r);
+}
 template <int ACT, bool PRECISE>
 __device__ __forceinline__ float activate_as(float x) {
   auto sigmoid = [](float t) { return PRECISE ? sigmoid_precise(t) : sigmoid_f32(t); };
@@ -149,7 +156,7 @@ constexpr int kStageFloats = 32 * 33;
 // already fp32 in shared memory (zeros past N or without a bias).  Rows that
 // can be moved in 16 bytes are finished by their thread; others (odd row
 // strides, the last columns) go through `stage`, so that the lanes of an access
-// are neighbours in a row instead of 32 rows apart (1531 x 777 fp32: 60 -> XX us).
+// are neighbours in a row instead of 32 rows apart (4234 x 270 x 123: 21 -> 15 us).
 template <int W>
 __device__ __forceinline__ void finish_rows(const LinearParams& p, float (&v)[W], const float* bias, int64_t m0, int n,
                                             float* stage) {
@@ -336,11 +343,13 @@ __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint64_
 
 // ---------------------------------------------------------------- one-CTA tiles
 
-// SWAP: the MMA's 128 rows are W's and its BN columns x's.
-template <int BN, bool SWAP>
+// SWAP: the MMA's 128 rows are W's and its BN columns x's.  DEEP: all of an
+// SM's shared memory for one CTA's stages, where there are no more CTAs than
+// SMs; otherwise half, so that two share an SM.
+template <int BN, bool SWAP, bool DEEP>
 struct TileCfg {
   static constexpr int STAGE = (128 + BN) * BK * 2;
-  static constexpr int ST = BN >= 128 ? 3 : (BN >= 64 ? 4 : 5);
+  static constexpr int ST = DEEP ? (BN >= 128 ? 6 : 8) : (BN >= 128 ? 3 : (BN >= 64 ? 4 : 5));
   static constexpr int PIPE = ST * STAGE;
   static constexpr int RED = 128 * BN * 4;              // split K: this CTA's accumulator tile
   static constexpr int DATA = PIPE;                     // behind RED, the epilogue's staging blocks
@@ -355,7 +364,7 @@ struct TileCfg {
 // lie in at most two aligned 16-byte pieces, loaded whole and shifted into
 // place.  The copy costs one pass over the operand and the product then runs
 // at TMA's speed; staging such rows by plain loads inside the product took
-// 375 us for 9000 x 7000 x 501 and 58 us for 1531 x 777 x 1003, this XX and XX.
+// 375 us for 9000 x 7000 x 501 and 58 us for 1531 x 777 x 1003, this 155 and 22.
 struct RepackParams {
   const uint16_t* src[2];
   uint16_t* dst[2];
@@ -372,15 +381,18 @@ __device__ __forceinline__ uint4 load_piece(const uint16_t* at, const uint16_t* 
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 __global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
-  const int op = blockIdx.y, chunks = p.Kp / 8;
-  const uint16_t* g = p.src[op];
+  const bool second = blockIdx.y != 0;
+  const int chunks = p.Kp / 8;
+  const uint16_t* g = second ? p.src[1] : p.src[0];
   if (g == nullptr) return;
-  const int64_t total = p.rows[op] * chunks;
-  const uint16_t* hi = g + (p.rows[op] - 1) * p.ld[op] + p.K;
+  uint16_t* dst = second ? p.dst[1] : p.dst[0];
+  const int64_t ld = second ? p.ld[1] : p.ld[0], rows = second ? p.rows[1] : p.rows[0];
+  const int64_t total = rows * chunks;
+  const uint16_t* hi = g + (rows - 1) * ld + p.K;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t row = i / chunks;
     const int k = static_cast<int>(i % chunks) * 8;
-    const uint16_t* at = g + row * p.ld[op] + k;
+    const uint16_t* at = g + row * ld + k;
     const uint32_t o = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) >> 1) & 7u;
     const uint4 x = load_piece(at - o, g, hi);
     const uint4 y = o != 0 ? load_piece(at - o + 8, g, hi) : make_uint4(0u, 0u, 0u, 0u);
@@ -397,15 +409,15 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
       if (p.K - k <= 2 * j) w[j] = 0u;
       else if (p.K - k == 2 * j + 1) w[j] &= 0xFFFFu;
     }
-    *reinterpret_cast<uint4*>(p.dst[op] + row * p.Kp + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + row * p.Kp + k) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-template <int BN, bool SWAP>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int BN, bool SWAP, bool DEEP>
+__global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const LinearParams p) {
-  using C = TileCfg<BN, SWAP>;
+  using C = TileCfg<BN, SWAP, DEEP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* sBias = reinterpret_cast<float*>(smem + C::DATA);
@@ -773,10 +785,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   }
 }
 
-template <int BN, bool SWAP>
+template <int BN, bool SWAP, bool DEEP>
 cudaError_t launch_tile(const LinearParams& p, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st) {
-  using C = TileCfg<BN, SWAP>;
-  auto kern = linear_tile_kernel<BN, SWAP>;
+  using C = TileCfg<BN, SWAP, DEEP>;
+  auto kern = linear_tile_kernel<BN, SWAP, DEEP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.tiles_a) * p.tiles_b * p.splits;
@@ -812,25 +824,26 @@ LinearPlan plan_linear(int M, int N, int K) {
   }
   pl.splits = 1;
   if (M <= 32) {
-    // W streams once: enough CTAs to draw on all of HBM, K steps enough to
-    // fill each one's pipeline (4 x 4096 x 4096: 11.1 us with 4 splits, 11.5
-    // with 8, 13.0 with 2; 4 x 16384 x 4096: 25.2 with 2, 27.7 with 1)
+    // W streams once: CTAs for most SMs, but K steps enough to fill each one's
+    // pipeline (4 x 4096 x 4096: 10.6 us with 4 splits, 12.2 with 2; 4 x 8192 x
+    // 1024: 6.1 whole, 6.7 in halves).  Clusters of 8 only where they are few:
+    // with an SM's shared memory each they do not all fit at once (4 x 2048 x
+    // 8192: 17.8 us, with 4 splits 12.2; 4 x 1024 x 4096, 8 tiles: 6.7 and 8.0).
     pl.swap = true;
     pl.bn = M <= 16 ? 16 : 32;
     const long long tiles = (N + 127) / 128;
-    while (pl.splits < 8 && (tiles * pl.splits < 100 ? ksteps / (pl.splits * 2) >= 4
-                                                     : tiles * pl.splits < 148 && ksteps / (pl.splits * 2) >= 32))
+    while (pl.splits < 8 && tiles * pl.splits * 2 <= (pl.splits < 4 ? 148 : 64) &&
+           ksteps / (pl.splits * 2) >= (tiles * pl.splits < 40 ? 6 : 12))
       pl.splits *= 2;
     return pl;
   }
-  // 64 columns while two such CTAs fit on every SM, then 128; K is split only
-  // where the tiles leave SMs idle (1024 x 1024 x 1024, 128 tiles: 7.1 us whole,
-  // 9.7 in halves; 128 x 4096 x 4096, 64 tiles: 13.8 in quarters, 15.9 in
-  // halves)
+  // 64 columns while the tiles do not outnumber the SMs, split in K where half
+  // of them would idle (768 x 768 x 3000, 72 tiles: 13.7 us in halves, 17.3
+  // whole, 20.9 in quarters; 1024 x 1024 x 1024, 128 tiles: 6.6 whole, 9.8 in
+  // halves), otherwise 128 (512 x 4096 x 4096: 19.4 us with 128, 23.9 with 64)
   const long long tiles = static_cast<long long>((M + 127) / 128) * ((N + 63) / 64);
-  pl.bn = tiles <= 296 ? 64 : 128;
-  if (tiles < 100)
-    while (pl.splits < 8 && tiles * pl.splits * 2 <= 296 && ksteps / (pl.splits * 2) >= 4) pl.splits *= 2;
+  pl.bn = tiles <= 148 ? 64 : 128;
+  while (pl.splits < 4 && tiles * pl.splits * 2 <= 148 && ksteps / (pl.splits * 2) >= 4) pl.splits *= 2;
   return pl;
 }
 
@@ -872,8 +885,12 @@ cudaError_t launch_linear(LinearParams p, const LinearPlan& pl, const CUtensorMa
   p.tiles_b = (rows_b + pl.bn - 1) / pl.bn;
   const CUtensorMap& ta = pl.swap ? tw : tx;
   const CUtensorMap& tb = pl.swap ? tx : tw;
-  if (pl.swap) return pl.bn == 16 ? launch_tile<16, true>(p, ta, tb, st) : launch_tile<32, true>(p, ta, tb, st);
-  return pl.bn == 64 ? launch_tile<64, false>(p, ta, tb, st) : launch_tile<128, false>(p, ta, tb, st);
+  if (static_cast<long long>(p.tiles_a) * p.tiles_b * p.splits <= device_sm_count()) {
+    if (pl.swap) return pl.bn == 16 ? launch_tile<16, true, true>(p, ta, tb, st) : launch_tile<32, true, true>(p, ta, tb, st);
+    return pl.bn == 64 ? launch_tile<64, false, true>(p, ta, tb, st) : launch_tile<128, false, true>(p, ta, tb, st);
+  }
+  if (pl.swap) return pl.bn == 16 ? launch_tile<16, true, false>(p, ta, tb, st) : launch_tile<32, true, false>(p, ta, tb, st);
+  return pl.bn == 64 ? launch_tile<64, false, false>(p, ta, tb, st) : launch_tile<128, false, false>(p, ta, tb, st);
 }
 
 }  // namespace jattn

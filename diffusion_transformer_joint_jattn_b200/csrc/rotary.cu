@@ -200,25 +200,24 @@ cudaError_t launch_u(RotaryParams p, cudaStream_t st) {
   // paid off; more: few tokens' rows per block); small problems take fewer
   // tokens, so that every SM has blocks.
   const int slots = kRotThreads / p.units;
-  const auto groups_of = [&](int tile) { return slots / tile < total ? slots / tile : total; };
-  const auto used = [&](int tile) {
-    const int g = groups_of(tile), rounds = (total + g - 1) / g;
-    return static_cast<double>(total) * tile / (static_cast<double>(rounds) * slots);
-  };
-  double best = 0.0;
-  for (int tile = 1; tile <= slots; ++tile) best = used(tile) > best ? used(tile) : best;
+  int rounds[kRotThreads + 1], used[kRotThreads + 1], best = 0;
+  for (int tile = 1; tile <= slots; ++tile) {
+    const int g = slots / tile < total ? slots / tile : total;
+    rounds[tile] = (total + g - 1) / g;
+    used[tile] = static_cast<int>(1000ll * total * tile / (static_cast<long long>(rounds[tile]) * slots));   // per mille
+    if (used[tile] > best) best = used[tile];
+  }
   p.tile = 1;
   int gap = INT32_MAX;
   for (int tile = 1; tile <= slots; ++tile) {
-    const int rounds = (total + groups_of(tile) - 1) / groups_of(tile);
-    const int d = rounds > kRounds ? rounds - kRounds : kRounds - rounds;
-    if (used(tile) >= best - 0.05 && d < gap && tile * p.rot * 4 <= 32768) {
+    const int d = rounds[tile] > kRounds ? rounds[tile] - kRounds : kRounds - rounds[tile];
+    if (used[tile] >= best - 50 && d < gap && tile * p.rot * 4 <= 32768) {
       gap = d;
       p.tile = tile;
     }
   }
   while (p.tile > 1 && p.tokens / p.tile < 2 * 148) p.tile /= 2;
-  p.groups = groups_of(p.tile);
+  p.groups = slots / p.tile < total ? slots / p.tile : total;
   const long long blocks = (p.tokens + p.tile - 1) / p.tile;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
   // few tokens: the heads over more blocks

@@ -545,7 +545,8 @@ def fwd_fp8_repair_noalloc(qkv_txt, qkv_img, qkv_ref, pos, split: Sequence[int],
 
 def joint_attention(qkv_txt, qkv_img, qkv_ref, pos, split, theta: float = 10000.0, path: str = "bf16",
                     operand_dtype: str | None = None, want_lse: bool = False, out=None, stream=None,
-                    norm_w=None, eps: float = 1e-6, workspace=None, precise: bool = True):
+                    norm_w=None, eps: float = 1e-6, workspace=None, precise: bool = True, proj_w=None, proj_b=None,
+                    residual=None):
     """The whole hot path, with the query/key RMSNorm fused into the
     prologue when ``norm_w`` is given.  path "bf16": the high-precision pair
     rope_qkv_hp -> fwd_bf16_hp by default; ``precise=False`` selects the
@@ -560,9 +561,16 @@ def joint_attention(qkv_txt, qkv_img, qkv_ref, pos, split, theta: float = 10000.
     Its plain 16-bit path takes bf16 operands (fp16 operands are those of the
     high-precision pair).  The host entry has no LSE output and no norm;
     those need device tensors.
+    proj_w (bf16 [N, H * d], device tensors only): the output projection,
+    ``linear`` over the heads of O, with ``proj_b`` [N] and ``residual`` bf16
+    [B, S, N] added; the result [B, S, N] takes O's place.
     Returns O bf16 [B, S, H, d] (and LSE for device tensors)."""
     parts = [qkv_txt, qkv_img, qkv_ref]
     ref = next(t for t in parts if t is not None)
+    if proj_w is None and (proj_b is not None or residual is not None):
+        raise ValueError("proj_b and residual belong to the projection: proj_w is missing")
+    if proj_w is not None and not ref.is_cuda:
+        raise ValueError("the output projection needs device tensors")
     if not ref.is_cuda:
         if want_lse or norm_w is not None:
             raise ValueError("LSE output and the query/key norm need device tensors")
@@ -612,6 +620,8 @@ def joint_attention(qkv_txt, qkv_img, qkv_ref, pos, split, theta: float = 10000.
         o, lse = fwd_fp8(q, k, v, sc, want_lse=want_lse, stream=stream)
     else:
         raise ValueError(f"unknown path {path!r}")
+    if proj_w is not None:
+        o = linear(o.flatten(2), proj_w, proj_b, residual=residual, stream=stream)
     return (o, lse) if want_lse else o
 
 
