@@ -90,7 +90,7 @@ struct __align__(8) Bars {
   uint64_t k_full[4], k_empty[4];
   uint64_t v_full[4], v_empty[4], v_ready[4];
   uint64_t s_full[2][2], p_full[2][2];                // [map][buffer]
-  uint64_t exchange[2];
+  uint64_t exchange[3];
   uint64_t turn[2][4];                                // [map][warp]
   Share share;
   uint32_t tmem_base;
@@ -393,7 +393,14 @@ enum : int {
   kBf16Split = 2,  // bf16 operands, P as the sum of two bf16: twice the P.V products, no second copy of V
 };
 
-template <int D, int KIND>
+// QUAD: a range of at most 32 rows (a few queries, one each in the single-token
+// form).  They stand four times in the Q tile, once in each quarter of 32 TMEM
+// lanes, so that the work on them can be spread over the four schedulers: map
+// 0's softmax is warp 0's, map 1's warp 5's (left in the same quarter, both
+// would be one scheduler's), and with kBf16Split the low parts of P are the
+// business of warps 2 and 7, in their own rows: one P.V product instead of
+// two, the two results added at the end.  The other softmax warps rest.
+template <int D, int KIND, bool QUAD>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const DiffParams p) {
@@ -431,10 +438,11 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int t = 0; t < 2; ++t) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bar->s_full[t][i], 1);
-        mbar_init(&bar->p_full[t][i], BM / 32);
+        mbar_init(&bar->p_full[t][i], !QUAD ? BM / 32 : (KIND == kBf16Split ? 2 : 1));
       }
-      mbar_init(&bar->exchange[t], 2 * BM);
+      mbar_init(&bar->exchange[t], !QUAD ? 2 * BM : (t == 0 ? 2 : 1));
     }
+    mbar_init(&bar->exchange[2], 1);
     for (int i = 0; i < 8; ++i) mbar_init(&bar->turn[0][i], 1);
     bar->abort = 0;
     fence_mbarrier_init();
@@ -472,15 +480,28 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (lane == 0) {
         int nq = 0, nk = 0;                             // Q tiles, key tiles (K and V) loaded so far
         bool v_behind = false;                          // the last key tile's V was not issued
+        bool lent = false;                              // QUAD: the Q tile serves the last segment's epilogue
+        uint32_t lent_phase = 0;
         Segment s;
         bool ok = true;
         for (Walk walk(p, share); ok && walk.next(p, share, s);) {
           if (s.n_kv == 0) continue;
           // the Q buffer is free once the previous segment's Q.K^T are done
           if (nq > 0 && !mbar_wait(&bar->q_empty, (nq - 1) & 1, ctl)) break;
+          if (QUAD && lent) {
+            if (!mbar_wait(&bar->exchange[2], lent_phase, ctl)) break;
+            lent_phase ^= 1u;
+          }
+          lent = s.whole;
           mbar_arrive_expect_tx(&bar->q_full, C::TB);
-          for (int x = 0; x < C::NBOX; ++x)
-            tma_load_4d(&tmQ, &bar->q_full, sQ + x * C::BOXB, x * 64, s.rt * BM, s.gi, s.b);
+          for (int x = 0; x < C::NBOX; ++x) {
+            if constexpr (QUAD) {
+              for (int k = 0; k < 4; ++k)
+                tma_load_4d(&tmQ, &bar->q_full, sQ + x * C::BOXB + k * 32 * 128, x * 64, 0, s.gi, s.b);
+            } else {
+              tma_load_4d(&tmQ, &bar->q_full, sQ + x * C::BOXB, x * 64, s.rt * BM, s.gi, s.b);
+            }
+          }
           ++nq;
           const int kvh = kv_head(s.gi);
           for (int j = 0; j < s.n_kv; ++j, ++nk) {
@@ -535,7 +556,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
           mma_ts_if(lead, tmem + col_o(t), tmem + col_s(t, buf) + kk * 8, vd + kk * 128, idesc_pv, acc || kk > 0);
-        if constexpr (KIND == kBf16Split) {
+        if constexpr (KIND == kBf16Split && !QUAD) {
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)                     // the low parts, in the columns behind
             mma_ts_if(lead, tmem + col_o(t), tmem + col_s(t, buf) + 32 + kk * 8, vd + kk * 128, idesc_pv, 1);
@@ -662,7 +683,10 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs_softmax<D>()));
     const int t = warp >> 2;                            // map of this warpgroup
-    const int row = (warp & 3) * 32 + lane;             // TMEM lane == row in the tile
+    // QUAD: the warp of this map that computes, and the one that has P's low parts
+    const bool hi_role = (warp & 3) == t, lo_role = KIND == kBf16Split && (warp & 3) == t + 2;
+    const bool works = !QUAD || hi_role || lo_role;
+    const int row = QUAD ? lane : (warp & 3) * 32 + lane;   // of the tile; TMEM lane (warp & 3) * 32 + lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t to = lane_base + col_o(t);
     const float c_j = p.scale_log2;
@@ -670,11 +694,11 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     uint32_t idx = 0, ex_phase = 0, turns = 0;
     Segment s;
     bool ok = true;
-    for (Walk walk(p, share); ok && walk.next(p, share, s);) {
+    for (Walk walk(p, share); works && ok && walk.next(p, share, s);) {
       const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(s.b) * p.S_kv : nullptr;
       const int r = s.rt * BM + row;                    // row of the range
       const bool live = r < p.R;
-      const bool warp_live = s.rt * BM + (warp & 3) * 32 < p.R;
+      const bool warp_live = QUAD || s.rt * BM + (warp & 3) * 32 < p.R;
       const int head = s.gi * p.hpg + (live ? r / p.S_q : 0), s_q = live ? r % p.S_q : 0;
       const int n = s.n_half, key0 = s.t0 * BN;
       // needed at the end; read while the first tiles are on their way
@@ -752,9 +776,11 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // The two warps of a scheduler (map 0's and map 1's of the same rows)
         // take the exponential unit in turns: left to themselves they fall into
         // step, want it at the same time and leave it idle at the same time.
-        ok = warp_wait(&bar->turn[t][warp & 3], (turns ^ (t ^ 1)) & 1, ctl);
-        if (!ok) break;
-        ++turns;
+        if constexpr (!QUAD) {
+          ok = warp_wait(&bar->turn[t][warp & 3], (turns ^ (t ^ 1)) & 1, ctl);
+          if (!ok) break;
+          ++turns;
+        }
         // no key so far: every probability is exp2(-inf) = 0
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
         const float2 c2 = make_float2(c_j, c_j), nm2 = make_float2(neg_m, neg_m);
@@ -771,10 +797,14 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if constexpr (KIND == kBf16Split)
             lo[c] = pack_x2<true>(e.x - __uint_as_float(pk[c] << 16), e.y - __uint_as_float(pk[c] & 0xFFFF0000u));
         }
+        if constexpr (KIND == kBf16Split && QUAD) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = lo_role ? lo[c] : pk[c];
+        }
         tmem_st32_issue(ts, pk);
-        if constexpr (KIND == kBf16Split) tmem_st32_issue(ts + 32, lo);
+        if constexpr (KIND == kBf16Split && !QUAD) tmem_st32_issue(ts + 32, lo);
         // passed earlier, among the last exponentials, it cost 3%
-        arrive_if(lane == 0, &bar->turn[t ^ 1][warp & 3]);
+        if constexpr (!QUAD) arrive_if(lane == 0, &bar->turn[t ^ 1][warp & 3]);
         tmem_wait_st();
         l_run += (acc0.x + acc0.y) + (acc1.x + acc1.y);
         if (mx != mx) l_run = mx;                       // NaN in, NaN out
@@ -798,7 +828,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // this part's normalised output and log-sum-exp of its map
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.from_start ? 1 : 0);
         if (warp_live) {
-          float* dst = p.part_o + ((slot * 2 + t) * BM + row) * D;
+          // QUAD: the low parts' product in rows 64 on, added by the merge
+          float* dst = p.part_o + ((slot * 2 + t) * BM + row + (QUAD && lo_role ? 64 : 0)) * D;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -812,9 +843,93 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                                 __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
             }
           }
-          if (live) p.part_l[(slot * 2 + t) * BM + row] = lse2;
+          if (live && !(QUAD && lo_role)) p.part_l[(slot * 2 + t) * BM + row] = lse2;
         }
         tc_fence_before();                              // before the next segment's P.V overwrites O_t
+        continue;
+      }
+      __nv_bfloat16* o_row = p.o + ((static_cast<size_t>(s.b) * p.S_q + s_q) * p.H + head) * D;
+      float* lse_row = p.lse != nullptr && live
+                           ? p.lse + static_cast<size_t>(t) * rows + (static_cast<size_t>(s.b) * p.H + head) * p.S_q + s_q
+                           : nullptr;
+      if constexpr (QUAD) {
+        if (lse_row != nullptr && hi_role) *lse_row = lse2 * 0.69314718055994531f;
+        if (n == 0) {                                   // no key: zeros, and no Q tile to lend
+          if (t == 0 && hi_role && live)
+            for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(o_row + c) = make_uint4(0u, 0u, 0u, 0u);
+          continue;
+        }
+        // The maps' rows lie in different lanes: they meet in the Q tile's
+        // memory, [map][channel][row], whose last use is over and which the
+        // producer does not load again before exchange[2].
+        float* meet = reinterpret_cast<float*>(sQ) + t * D * 32 + lane;
+        if (lo_role) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t x[32];
+            tmem_ld32(to + c, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) meet[(c + e) * 32] = __uint_as_float(x[e]);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          tc_fence_before();
+          __syncwarp();
+          arrive_if(lane == 0, &bar->exchange[0]);
+          continue;
+        }
+        if constexpr (KIND == kBf16Split) {
+          ok = warp_wait(&bar->exchange[0], ex_phase, ctl);
+          if (!ok) break;
+        }
+        const float w = t == 0 ? inv : -lam * inv;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t x[32];
+          __syncwarp();
+          tmem_ld32(to + c, x);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float low = KIND == kBf16Split ? meet[(c + e) * 32] : 0.f;
+            meet[(c + e) * 32] = (__uint_as_float(x[e]) + low) * w;
+          }
+        }
+        tc_fence_before();
+        if (t == 1) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          arrive_if(lane == 0, &bar->exchange[1]);
+        } else {
+          ok = warp_wait(&bar->exchange[1], ex_phase, ctl);
+          if (!ok) break;
+          float sq = 0.f;
+#pragma unroll 8
+          for (int c = 0; c < D; ++c) {
+            const float x = meet[c * 32] + meet[(D + c) * 32];
+            sq = fmaf(x, x, sq);
+          }
+          const float f = p.norm_w != nullptr ? rsqrtf(sq * (1.f / D) + p.eps) * (1.f - p.lambda_init) : 1.f;
+          if (live) {
+#pragma unroll 2
+            for (int c = 0; c < D; c += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float a = (meet[(c + 2 * e) * 32] + meet[(D + c + 2 * e) * 32]) * f;
+                float b = (meet[(c + 2 * e + 1) * 32] + meet[(D + c + 2 * e + 1) * 32]) * f;
+                if (p.norm_w != nullptr) {
+                  a *= __ldg(p.norm_w + c + 2 * e);
+                  b *= __ldg(p.norm_w + c + 2 * e + 1);
+                }
+                y[e] = pack_x2<true>(a, b);
+              }
+              *reinterpret_cast<uint4*>(o_row + c) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          arrive_if(lane == 0, &bar->exchange[2]);
+        }
+        ex_phase ^= 1u;
         continue;
       }
       sL[t * BM + row] = inv;
@@ -863,7 +978,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
       }
       if (live) {
-        __nv_bfloat16* dst = p.o + ((static_cast<size_t>(s.b) * p.S_q + s_q) * p.H + head) * D + t * DM;
+        __nv_bfloat16* dst = o_row + t * DM;
         uint32_t w[DM / 2];
 #pragma unroll
         for (int e = 0; e < DM / 2; ++e) w[e] = pack_x2<true>(o[2 * e], o[2 * e + 1]);
@@ -879,9 +994,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           for (int e = 0; e < DM / 2; e += 4)
             *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
         }
-        if (p.lse != nullptr)
-          p.lse[static_cast<size_t>(t) * rows + (static_cast<size_t>(s.b) * p.H + head) * p.S_q + s_q] =
-              lse2 * 0.69314718055994531f;
+        if (lse_row != nullptr) *lse_row = lse2 * 0.69314718055994531f;
       }
     }
   }
@@ -966,7 +1079,7 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
         tot += w;
         const float* src = p.part_o + at * D + lane * E;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, src[e], acc[e]);
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, src[e] + (p.low_rows ? src[64 * D + e] : 0.f), acc[e]);
       }
     }
     const float inv = mx == -INFINITY ? 0.f : 1.f / tot;
@@ -992,12 +1105,12 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   for (int e = 0; e < E / 2; ++e) dst[e] = pack_x2<true>(out[2 * e], out[2 * e + 1]);
 }
 
-template <int D, int KIND>
+template <int D, int KIND, bool QUAD = false>
 cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   using C = Cfg<D>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
-  auto kern = diff_attn_kernel<D, KIND>;
+  auto kern = diff_attn_kernel<D, KIND, QUAD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   if (KIND == kBf16WideV && p.S_kv > 0) {
@@ -1025,6 +1138,11 @@ cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorM
 template <int D>
 cudaError_t launch_d(const DiffParams& p, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, cudaStream_t st) {
+  if (p.R <= kQuadRows) {
+    DiffParams q = p;
+    q.low_rows = in_bf16;
+    return in_bf16 ? launch_t<D, kBf16Split, true>(q, tq, tk, tv, st) : launch_t<D, kF16, true>(q, tq, tk, tv, st);
+  }
   if (!in_bf16) return launch_t<D, kF16>(p, tq, tk, tv, st);
   return p.v16 != nullptr ? launch_t<D, kBf16WideV>(p, tq, tk, tv, st) : launch_t<D, kBf16Split>(p, tq, tk, tv, st);
 }
@@ -1069,6 +1187,7 @@ bool diff_widens_v(int n_rt) { return n_rt >= 4; }
 
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st) {
+  static_assert(kQuadRows == 32, "one quarter of the TMEM lanes");
   return d == 128 ? launch_d<128>(p, in_bf16, tq, tk, tv, st) : launch_d<64>(p, in_bf16, tq, tk, tv, st);
 }
 

@@ -206,6 +206,7 @@ struct DiffParams {
   long long items_whole;        // the items below this number are walked whole, the others shared by all CTAs
   int ctas;                     // of the walk
   int merge;                    // items are shared: parts to merge
+  int low_rows;                 // set by the launcher: the parts' rows 64 on hold the products of P's low parts
   float scale_log2;
   const float* lam;             // [4][H][d / 2]
   float lambda_init;
@@ -230,7 +231,9 @@ struct DiffWalk {
 };
 DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms);
 bool diff_widens_v(int n_rt);
-// The maps describe (d, rows, heads or ranges, batch) with boxes of 64 x 128.
+// Ranges of at most this many rows are walked by a kernel of their own.
+constexpr int kQuadRows = 32;
+// The maps describe (d, rows, heads or ranges, batch) with boxes of 64 x 128 (q's: 64 x 32 where R <= kQuadRows).
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st);
 

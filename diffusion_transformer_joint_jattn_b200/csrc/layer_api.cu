@@ -29,16 +29,16 @@ bool matrix_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, in
   return jattn::encode_map16(m, base, 2, dims, strides, box);
 }
 
-// (d, rows, heads, batch) map of 16-bit elements, boxes of 64 channels x 128
-// rows; a dimension of one element gets a harmless stride.
+// (d, rows, heads, batch) map of 16-bit elements, boxes of 64 channels x
+// box_rows rows; a dimension of one element gets a harmless stride.
 bool heads_map(CUtensorMap* m, const void* base, int d, int64_t rows, int64_t heads, int64_t batch, int64_t row_stride,
-               int64_t head_stride, int64_t batch_stride) {
+               int64_t head_stride, int64_t batch_stride, int box_rows = 128) {
   const uint64_t dims[4] = {static_cast<uint64_t>(d), static_cast<uint64_t>(rows), static_cast<uint64_t>(heads),
                             static_cast<uint64_t>(batch)};
   const uint64_t strides[3] = {static_cast<uint64_t>(rows > 1 ? row_stride : d) * 2,
                                static_cast<uint64_t>(heads > 1 ? head_stride : d) * 2,
                                static_cast<uint64_t>(batch > 1 ? batch_stride : d) * 2};
-  const uint32_t box[4] = {64u, 128u, 1u, 1u};
+  const uint32_t box[4] = {64u, static_cast<uint32_t>(box_rows), 1u, 1u};
   return jattn::encode_map16(m, base, 4, dims, strides, box);
 }
 
@@ -331,7 +331,8 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   const int64_t D = s->d, contiguous[3] = {s->H_kv * skv * D, skv * D, D};
   const int64_t* vs = widen ? contiguous : s->v_stride;
   if (widen) vb = p.v16;
-  if (!heads_map(&tq, q, s->d, r.R, r.n_groups, s->B, r.row_stride, r.group_stride, s->q_stride[0]) ||
+  if (!heads_map(&tq, q, s->d, r.R, r.n_groups, s->B, r.row_stride, r.group_stride, s->q_stride[0],
+                 r.R <= jattn::kQuadRows ? jattn::kQuadRows : 128) ||
       !heads_map(&tk, kb, s->d, skv, s->H_kv, s->B, s->k_stride[2], s->k_stride[1], s->k_stride[0]) ||
       !heads_map(&tv, vb, s->d, skv, s->H_kv, s->B, vs[2], vs[1], vs[0]))
     return JATTN_ERR_CUDA;

@@ -71,6 +71,24 @@ def test_lengths(cuda_device, S_q, S_kv):
     assert (o[0] == 0).all() and torch.isneginf(lse[:, 0]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S_q", [1, 9, 16, 17])
+def test_many_sequences(cuda_device, dtype, d, S_q):
+    """More ranges than SMs over caches of unequal length, empty ones among
+    them: a CTA walks whole ranges and parts of others in one go.  16 queries
+    of two heads are the 32 rows of the few-row kernel, 17 are past it."""
+    B, S_kv = 80, 1100
+    q, k, v, lam, w = make(cuda_device, dtype, B, 4, 2, S_q, S_kv, d, seed=S_q)
+    lens = np.random.default_rng(S_q).integers(0, S_kv + 1, B)
+    lens[[3, 4, 41, 79]] = 0, 0, S_kv, 0
+    allowed = np.arange(S_kv)[None] < lens[:, None]
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    for norm in (w, None):
+        o, lse = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=norm, eps=EPS, kv_len=n, want_lse=True)
+        check(o, lse, q, k, v, lam, norm, allowed)
+
+
 @pytest.mark.parametrize("S_q", [1, 200])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -3.0e38])
 def test_key_mask(cuda_device, S_q, bad):
