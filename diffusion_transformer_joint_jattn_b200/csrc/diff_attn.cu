@@ -221,6 +221,11 @@ __device__ __forceinline__ int v_exponent(uint32_t amax_bits) {
   return amax_bits == 0u ? 0 : min(max(static_cast<int>(amax_bits >> 23) - 127 - 14, -126), 126);
 }
 
+template <int E>
+struct alignas(4 * E) Vec4or2 {
+  float e[E];
+};
+
 // V's largest finite magnitude per (batch entry, K/V head) over its allowed
 // keys, then its fp16 copy, zeros at masked keys: 8 channels of a row per
 // thread and step, blockIdx.y = the head, kConvRows rows per block.
@@ -452,6 +457,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tmem_alloc(&bar->tmem_base, kTmemCols);
     tmem_relinquish();
   }
+  if (warp == kProducerWarp && lane < 3) tma_prefetch_desc(lane == 0 ? &tmQ : (lane == 1 ? &tmK : &tmV));
   if (warp == kShareWarp) {
     Share mine{0, 0, 0};
     if (p.items > p.items_whole) {
@@ -1010,15 +1016,20 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Merge of the items that several CTAs shared, one warp per query row: each
-// map's parts weighted by 2^(lse_part - lse), then the difference and the
-// norm.  blockIdx.x + 1 = a CTA of the walk; the first whose share starts
-// inside an item answers for that item.
-template <int D>
+// Merge of the items that several CTAs shared: each map's parts weighted by
+// 2^(lse_part - lse), then the difference and the norm.  blockIdx.x + 1 = a CTA
+// of the walk; the first whose share starts inside an item answers for that
+// item.  WPR warps per query row take the parts in turns (a single-token call
+// has few rows and up to a part per CTA, the tail of a long prompt many rows
+// of two or three parts); sums in a fixed order.
+constexpr int kMergeParts = 4;                          // loads in flight per warp and map
+template <int D, int WPR>
 __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int ctas) {
   constexpr int E = D / 32;                             // channels per lane
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+  using Chunk = Vec4or2<E>;
+  __shared__ float sums[4][2][D + 1];                   // [warp][map]: weighted outputs, weights
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const int row = (blockIdx.y * 4 + warp) / WPR;
   const int cta = blockIdx.x + 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long total = shared_prefix(p, p.B);
@@ -1031,7 +1042,7 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   const int per = p.n_groups * p.n_rt;
   const int b = static_cast<int>(item / per), gi = static_cast<int>(item / p.n_rt % p.n_groups);
   const int r = static_cast<int>(item % p.n_rt) * BM + row;
-  if (r >= p.R) return;
+  if (r >= p.R) return;                                 // WPR 4: the whole block
   const long long end = g - off + tiles_of(p, b);       // the item's last tile + 1
   int last = cta;                                       // the last CTA that has a part of it
   while (last + 1 < ctas && share_start(total, last + 1, ctas) < end) ++last;
@@ -1044,6 +1055,68 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
     const size_t slot = i == 0 ? 2 * static_cast<size_t>(cta - 1) + 1 : 2 * static_cast<size_t>(cta + i - 1);
     return (slot * 2 + t) * BM + row;
   };
+  float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    for (int i = lane; i < parts; i += 32) {
+      const float l = p.part_l[part_at(i, t)];
+      mx[t] = l > mx[t] || l != l ? l : mx[t];          // a NaN stays
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float l = __shfl_xor_sync(0xffffffffu, mx[t], o);
+      mx[t] = l > mx[t] || l != l ? l : mx[t];
+    }
+  }
+  float acc[2][E], tot[2] = {0.f, 0.f};
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[t][e] = 0.f;
+  for (int i0 = sub; i0 < parts; i0 += WPR * kMergeParts) {
+    Chunk x[kMergeParts][2], y[kMergeParts][2];
+    float w[kMergeParts][2];
+#pragma unroll
+    for (int k = 0; k < kMergeParts; ++k) {
+      const int i = min(i0 + k * WPR, parts - 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const size_t at = part_at(i, t);
+        const float l = p.part_l[at];
+        // a part without keys, or no part: weight 0
+        w[k][t] = i0 + k * WPR < parts && l != -INFINITY ? ex2_approx(l - mx[t]) : 0.f;
+        x[k][t] = *reinterpret_cast<const Chunk*>(p.part_o + at * D + lane * E);
+        if (p.low_rows) y[k][t] = *reinterpret_cast<const Chunk*>(p.part_o + (at + 64) * D + lane * E);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMergeParts; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (w[k][t] == 0.f) continue;                   // its output may be unwritten
+        tot[t] += w[k][t];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          acc[t][e] = fmaf(w[k][t], x[k][t].e[e] + (p.low_rows ? y[k][t].e[e] : 0.f), acc[t][e]);
+      }
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) sums[warp][t][lane * E + e] = acc[t][e];
+      if (lane == 0) sums[warp][t][D] = tot[t];
+    }
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      for (int k = 1; k < WPR; ++k) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[t][e] += sums[warp + k][t][lane * E + e];
+        tot[t] += sums[warp + k][t][D];
+      }
+  }
   float a1 = 0.f, a2 = 0.f;
   const size_t plane = static_cast<size_t>(p.H) * (D / 2);
   for (int i = lane; i < D / 2; i += 32) {
@@ -1059,36 +1132,14 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   const float lam = expf(a1) - expf(a2) + p.lambda_init;
   float out[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = 0.f;
-#pragma unroll
   for (int t = 0; t < 2; ++t) {
-    float mx = -INFINITY;
-    for (int s = 0; s < parts; ++s) {
-      const float l = p.part_l[part_at(s, t)];
-      mx = l > mx || l != l ? l : mx;                   // a NaN stays
-    }
-    float acc[E], tot = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (mx != -INFINITY) {
-      for (int s = 0; s < parts; ++s) {
-        const size_t at = part_at(s, t);
-        const float l = p.part_l[at];
-        if (l == -INFINITY) continue;
-        const float w = ex2_approx(l - mx);
-        tot += w;
-        const float* src = p.part_o + at * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, src[e] + (p.low_rows ? src[64 * D + e] : 0.f), acc[e]);
-      }
-    }
-    const float inv = mx == -INFINITY ? 0.f : 1.f / tot;
+    const float inv = mx[t] == -INFINITY ? 0.f : 1.f / tot[t];
     const float f = t == 0 ? inv : -lam * inv;
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = fmaf(f, acc[e], out[e]);
+    for (int e = 0; e < E; ++e) out[e] = t == 0 ? f * acc[0][e] : fmaf(f, acc[1][e], out[e]);
     if (p.lse != nullptr && lane == 0)
       p.lse[static_cast<size_t>(t) * rows + rg] =
-          mx == -INFINITY ? -INFINITY : (mx + __log2f(tot)) * 0.69314718055994531f;
+          mx[t] == -INFINITY ? -INFINITY : (mx[t] + __log2f(tot[t])) * 0.69314718055994531f;
   }
   if (p.norm_w != nullptr) {
     float sq = 0.f;
@@ -1121,7 +1172,8 @@ cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorM
   }
   kern<<<p.ctas, kThreads, C::SMEM, st>>>(tq, tk, tv, p);
   if ((e = cudaGetLastError()) != cudaSuccess || !p.merge) return e;
-  const dim3 grid(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>(((p.R < BM ? p.R : BM) + 3) / 4));
+  constexpr int WPR = QUAD ? 4 : 1;
+  const dim3 grid(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>(((p.R < BM ? p.R : BM) * WPR + 3) / 4));
   // launched while the walk runs (it waits for its end before it reads)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -1132,7 +1184,7 @@ cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorM
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, diff_merge_kernel<D>, p, p.ctas);
+  return cudaLaunchKernelEx(&cfg, diff_merge_kernel<D, WPR>, p, p.ctas);
 }
 
 template <int D>
