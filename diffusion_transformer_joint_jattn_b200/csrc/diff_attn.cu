@@ -284,6 +284,12 @@ __device__ __forceinline__ float lambda_of(const DiffParams& p, int head, int dm
   return expf(s1) - expf(s2) + p.lambda_init;
 }
 
+// a / b of non-negative numbers, almost always small ones (64-bit divisions
+// cost a microsecond each few).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 // Key tiles of an item of batch entry b; an empty one counts as one tile, so
 // that some CTA writes its zeros.
 __device__ __forceinline__ int tiles_of(const DiffParams& p, int b) { return max((key_count(p, b) + BN - 1) / BN, 1); }
@@ -331,11 +337,22 @@ __device__ __forceinline__ void locate(const DiffParams& p, long long g, long lo
   }
   const long long per = static_cast<long long>(p.n_groups) * p.n_rt;
   const int nt = tiles_of(p, b);
-  item = max(b * per, p.items_whole) + g / nt;
-  off = static_cast<int>(g % nt);
+  const long long n = divide(g, nt);
+  item = max(b * per, p.items_whole) + n;
+  off = static_cast<int>(g - n * nt);
 }
-// First of the `total` shared tiles that CTA c takes.
-__device__ __forceinline__ long long share_start(long long total, int c, int ctas) { return total * c / ctas; }
+// The `total` shared tiles in equal runs, one more for the first CTAs.
+struct Runs {
+  long long q;
+  int rem;
+  __device__ __forceinline__ Runs(long long total, int ctas) : q(divide(total, ctas)), rem(static_cast<int>(total - q * ctas)) {}
+  __device__ __forceinline__ long long start(int c) const { return c * q + min(c, rem); }
+  // The CTA that has tile g.
+  __device__ __forceinline__ int owner(long long g) const {
+    const long long head = rem * (q + 1);
+    return static_cast<int>(g < head ? divide(g, q + 1) : rem + divide(g - head, q));
+  }
+};
 
 // One piece of work: key tiles [t0, t0 + n_kv) of an item.
 struct Segment {
@@ -344,8 +361,8 @@ struct Segment {
 };
 __device__ __forceinline__ Segment segment_of(const DiffParams& p, long long item, int t0, int n, int nt) {
   Segment s;
-  s.rt = static_cast<int>(item % p.n_rt);
-  const int g = static_cast<int>(item / p.n_rt);
+  const int g = static_cast<int>(divide(item, p.n_rt));
+  s.rt = static_cast<int>(item - static_cast<long long>(g) * p.n_rt);
   s.gi = g % p.n_groups;
   s.b = g / p.n_groups;
   s.len = key_count(p, s.b);
@@ -370,7 +387,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool next(const DiffParams& p, const Share& share, Segment& s) {
     if (!whole && left <= 0) return false;
-    const int nt = tiles_of(p, static_cast<int>(item / (p.n_groups * p.n_rt)));
+    const int nt = tiles_of(p, static_cast<int>(divide(item, p.n_groups * p.n_rt)));
     const int n = whole ? nt : static_cast<int>(min(static_cast<long long>(nt - off), left));
     s = segment_of(p, item, off, n, nt);
     if (whole) {
@@ -462,7 +479,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     Share mine{0, 0, 0};
     if (p.items > p.items_whole) {
       const long long total = shared_prefix(p, p.B);
-      const long long g0 = share_start(total, blockIdx.x, gridDim.x), g1 = share_start(total, blockIdx.x + 1, gridDim.x);
+      const Runs runs(total, gridDim.x);
+      const long long g0 = runs.start(blockIdx.x), g1 = runs.start(blockIdx.x + 1);
       mine.count = g1 - g0;
       if (g1 > g0) locate(p, g0, mine.item, mine.off);
     }
@@ -473,6 +491,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
   const Share share = bar->share;
+  // the merge may find its rows on idle SMs meanwhile
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const WaitCtl ctl{&bar->abort, p.status, p.timeout_ns};
   auto kv_head = [&](int gi) { return static_cast<int>(static_cast<long long>(gi) * p.H_kv / p.n_groups); };
   // V rows of masked keys have to be zeroed: a mask, or a length inside the
@@ -1013,7 +1033,6 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Merge of the items that several CTAs shared: each map's parts weighted by
@@ -1031,22 +1050,19 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
   const int row = (blockIdx.y * 4 + warp) / WPR;
   const int cta = blockIdx.x + 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long total = shared_prefix(p, p.B);
-  const long long g = share_start(total, cta, ctas);
+  const Runs runs(total, ctas);
+  const long long g = runs.start(cta);
   if (g >= total) return;
   long long item;
   int off;
   locate(p, g, item, off);
-  if (off == 0 || share_start(total, cta - 1, ctas) > g - off) return;
-  const int per = p.n_groups * p.n_rt;
-  const int b = static_cast<int>(item / per), gi = static_cast<int>(item / p.n_rt % p.n_groups);
-  const int r = static_cast<int>(item % p.n_rt) * BM + row;
+  if (off == 0 || runs.start(cta - 1) > g - off) return;
+  const int range = static_cast<int>(divide(item, p.n_rt)), b = range / p.n_groups, gi = range % p.n_groups;
+  const int r = static_cast<int>(item - static_cast<long long>(range) * p.n_rt) * BM + row;
   if (r >= p.R) return;                                 // WPR 4: the whole block
-  const long long end = g - off + tiles_of(p, b);       // the item's last tile + 1
-  int last = cta;                                       // the last CTA that has a part of it
-  while (last + 1 < ctas && share_start(total, last + 1, ctas) < end) ++last;
-  const int parts = last - cta + 2;
+  // the last CTA that has a part of the item, by its last tile
+  const int parts = runs.owner(g - off + tiles_of(p, b) - 1) - cta + 2;
   const int head = gi * p.hpg + r / p.S_q, s_q = r % p.S_q;
   const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
   const size_t rg = (static_cast<size_t>(b) * p.H + head) * p.S_q + s_q;
@@ -1055,6 +1071,8 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
     const size_t slot = i == 0 ? 2 * static_cast<size_t>(cta - 1) + 1 : 2 * static_cast<size_t>(cta + i - 1);
     return (slot * 2 + t) * BM + row;
   };
+  // everything above is the inputs' alone: the parts from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int t = 0; t < 2; ++t) {

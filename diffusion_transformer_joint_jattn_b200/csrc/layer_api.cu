@@ -100,6 +100,10 @@ DiffLayout diff_layout(const jattn_diff_shape* s, const DiffRanges& r, bool in_b
   return L;
 }
 
+bool linear_sizes(const jattn_linear_shape* s) {
+  const int32_t most = 1 << 30;
+  return s != nullptr && s->M >= 0 && s->M <= most && s->N >= 0 && s->N <= most && s->K >= 1 && s->K <= most;
+}
 int64_t padded(int64_t k) { return (k + 7) / 8 * 8; }
 
 // Which operands of the linear layer TMA cannot address (one row needs no
@@ -173,7 +177,7 @@ jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors,
       p.ys[t][i] = x.y_stride[i];
     }
   }
-  if (heads * parts > INT32_MAX) return JATTN_ERR_INVALID_ARG;
+  if (heads * parts > (1 << 24)) return JATTN_ERR_INVALID_ARG;
   if (B == 0 || S == 0 || heads == 0) return JATTN_OK;
   if (pos == nullptr || freqs == nullptr) return JATTN_ERR_INVALID_ARG;
   if (!aligned(pos, 4) || !aligned(freqs, 8)) return JATTN_ERR_ALIGNMENT;
@@ -197,13 +201,13 @@ jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors,
 }
 
 size_t jattn_linear_workspace(const jattn_linear_shape* s, const void* x, const void* w) {
-  if (s == nullptr || s->M < 0 || s->N < 0 || s->K < 1) return 0;
+  if (!linear_sizes(s)) return 0;
   return linear_copies(s, x, w).total;
 }
 
 jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void* w, const void* bias,
                           const void* residual, void* y, void* workspace, size_t workspace_bytes, void* stream) {
-  if (s == nullptr || s->M < 0 || s->N < 0 || s->K < 1) return JATTN_ERR_INVALID_ARG;
+  if (!linear_sizes(s)) return JATTN_ERR_INVALID_ARG;
   if (!is_16bit(s->in_dtype) || !is_float(s->out_dtype)) return JATTN_ERR_UNSUPPORTED;
   if (bias != nullptr && !is_float(s->bias_dtype)) return JATTN_ERR_UNSUPPORTED;
   if (s->act < JATTN_ACT_NONE || s->act > JATTN_ACT_RELU) return JATTN_ERR_UNSUPPORTED;

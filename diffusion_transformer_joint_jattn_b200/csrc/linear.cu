@@ -67,12 +67,12 @@ __device__ __forceinline__ void store_from_f32(void* p, int64_t i, int dt, float
 __device__ __forceinline__ float sigmoid_f32(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 // For fp32 outputs: exp to 2 ulp, the reciprocal with one Newton step (without
 // the branches of a division, which kept the elements of a row from
-// interleaving: 8 us on a 128 x 128 tile).  Below -87, where x sigmoid(x) is
-// under 2^-118, exp stays at e^87 so that the reciprocal stays normal.
+// interleaving: 8 us on a 128 x 128 tile).  Below -87 the reciprocal is no
+// normal number: 0.
 __device__ __forceinline__ float sigmoid_precise(float x) {
   const float d = 1.f + expf(fminf(-x, 87.f));
   const float r = __fdividef(1.f, d);
-  return fmaf(r, fmaf(-d, r, 1.f), r);
+  return x < -87.f ? 0.f : fmaf(r, fmaf(-d, r, 1.f), r);
 }
 template <int ACT, bool PRECISE>
 __device__ __forceinline__ float activate_as(float x) {

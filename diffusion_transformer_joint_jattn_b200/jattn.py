@@ -636,6 +636,8 @@ def _elsewhere(call, dev: int, stream, tensors):
     """``call()`` with the tensors' device current and on ``stream`` (that
     device's current one when None).  The outputs are allocated for that
     stream, and the tensors are kept from reuse until its work is done."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream is one of {stream.device}, the tensors are on cuda:{dev}")
     with torch.cuda.device(dev):
         if stream is None or stream == torch.cuda.current_stream():
             return call()

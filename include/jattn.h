@@ -398,7 +398,8 @@ typedef struct {
  *   inverse   : 0, or nonzero for the transposed map (turned by -t): the
  *               gradient with respect to x is the inverse of that of y.
  * Errors: JATTN_ERR_INVALID_ARG, JATTN_ERR_UNSUPPORTED (dtype),
- * JATTN_ERR_ALIGNMENT.  B or S or every H of 0 is no work and JATTN_OK.
+ * JATTN_ERR_ALIGNMENT.  Heads times parts of all tensors up to 2^24.  B or S
+ * or every H of 0 is no work and JATTN_OK.
  */
 jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors, jattn_dtype dtype, int32_t B,
                           int32_t S, int32_t d, int32_t parts, int32_t rot, const int32_t* pos,
@@ -415,8 +416,8 @@ typedef enum {
   JATTN_ACT_RELU = 4
 } jattn_act;
 
-/* Row strides ldx, ldw >= K and ldy, ldr >= N in elements.  M, N in [0, 2^31),
- * K in [1, 2^31). */
+/* Row strides ldx, ldw >= K and ldy, ldr >= N in elements, below 2^38.  M, N
+ * in [0, 2^30], K in [1, 2^30]. */
 typedef struct {
   int32_t M, N, K;
   int64_t ldx, ldw, ldy, ldr;

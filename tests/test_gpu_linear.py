@@ -107,6 +107,27 @@ def test_infinities_stay_in_their_rows(cuda_device):
         assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("out", ["fp16", "fp32"])
+def test_activations_at_the_ends(cuda_device, out):
+    """x = value * 1: the activation of values far out, where exp leaves the
+    fp32 range.  Expected from fp64; what vanishes there is 0 here."""
+    vals = torch.tensor([0.0, -0.5, 0.5, -20.0, 20.0, -86.0, -87.5, -90.0, -200.0, 200.0, -6e4, 6e4, -1e30, 1e30, -3e38, 3e38,
+                         float("nan")])
+    x = vals.bfloat16().view(-1, 1).to(cuda_device)
+    w = torch.ones(40, 1, dtype=torch.bfloat16, device=cuda_device)
+    ref64 = x.double().cpu()
+    for act, f in (("gelu", torch.nn.functional.gelu), ("silu", torch.nn.functional.silu), ("relu", torch.relu),
+                   ("gelu_tanh", lambda v: torch.nn.functional.gelu(v, approximate="tanh"))):
+        want = f(ref64).to(DT[out]).double().expand(-1, 40)
+        got = jattn.linear(x, w, act=act, out_dtype=DT[out]).double().cpu()
+        assert torch.equal(got.isnan(), want.isnan()), act
+        fine = want.isfinite()
+        assert torch.equal(got[~fine & ~want.isnan()], want[~fine & ~want.isnan()]), act
+        # half a step of the type, the epilogue's 2^-18, and what fp32 cannot hold
+        tol = (torch.finfo(DT[out]).eps + 2.0 ** -18) * want[fine].abs() + max(torch.finfo(DT[out]).tiny, 2.0 ** -110)
+        assert ((got[fine] - want[fine]).abs() <= tol).all(), (act, got[:, 0], want[:, 0])
+
+
 def test_same_bits_every_time(cuda_device):
     for M, N, K in ((4, 512, 4096), (100, 256, 2048), (2500, 2700, 264)):
         x, w, b, _ = make(cuda_device, "fp16", M, N, K)

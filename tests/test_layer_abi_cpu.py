@@ -26,7 +26,8 @@ def test_rotary_refusals():
     for kw in (dict(n=0), dict(n=3), dict(B=-1), dict(S=-1), dict(d=0), dict(parts=0), dict(parts=3), dict(d=6, parts=2, rot=2),
                dict(rot=0), dict(rot=3), dict(rot=66), dict(d=1032, rot=64), dict(layout=2), dict(scale=float("nan")),
                dict(scale=float("inf")), dict(split=(16, 24, 22)), dict(split=(15, 25, 24)), dict(split=(-2, 42, 24)),
-               dict(x=None), dict(y=None), dict(pos=None), dict(freqs=None), dict(H=-1)):
+               dict(x=None), dict(y=None), dict(pos=None), dict(freqs=None), dict(H=-1),
+               dict(H=(1 << 24) + 1), dict(H=(1 << 23) + 1, parts=2, rot=32)):
         rotary(INV, **kw)
     rotary(UNS, dtype=jattn.E4M3)
     rotary(UNS, dtype=9)
@@ -50,7 +51,8 @@ def linear(code, **kw):
 
 def test_linear_refusals():
     for kw in (dict(M=-1), dict(N=-1), dict(K=0), dict(ldx=15), dict(ldw=8), dict(ldy=7), dict(res=A, ldr=7), dict(x=None),
-               dict(w=None), dict(y=None), dict(res=A, y=A, ldy=16), dict(ldx=1 << 38)):
+               dict(w=None), dict(y=None), dict(res=A, y=A, ldy=16), dict(ldx=1 << 38),
+               dict(M=(1 << 30) + 1), dict(N=(1 << 30) + 1, ldy=1 << 31), dict(K=(1 << 30) + 1, ldx=1 << 31, ldw=1 << 31)):
         linear(INV, **kw)
     for kw in (dict(i=jattn.FP32), dict(i=jattn.E4M3), dict(o=jattn.E4M3), dict(bias=A, b=jattn.E4M3), dict(act=5), dict(act=-1)):
         linear(UNS, **kw)
