@@ -169,9 +169,10 @@ cudaError_t launch_rotary(const RotaryParams& p, int dtype, bool half, cudaStrea
 
 // Linear layer y = act(x w^T + bias) + residual.
 struct LinearPlan {
-  bool pair;                    // 256 x 256 tiles by CTA pairs
+  bool pair;                    // 256 x bn tiles by CTA pairs
+  bool flush;                   // accumulators emptied into registers on the way
   bool swap;                    // few rows: W's rows are the MMA's rows
-  int bn, splits;               // of the one-CTA tiles
+  int bn, splits;               // columns of a tile; parts of K of the one-CTA tiles
 };
 struct LinearParams {
   int M, N, K;
@@ -186,9 +187,9 @@ struct LinearParams {
   int tiles_a, tiles_b, splits;
   int vec_y, vec_r;             // bytes of the widest aligned access of y's and residual's rows, 0 = elements
 };
-LinearPlan plan_linear(int M, int N, int K);
+LinearPlan plan_linear(int M, int N, int K, bool out_f32);
 // tx, tw: 2-D maps with 64-element boxes of plan.pair ? 128 : (swap ? bn : 128) rows of x and
-// plan.pair ? 128 : (swap ? 128 : bn) rows of w.
+// plan.pair ? bn / 2 : (swap ? 128 : bn) rows of w.
 cudaError_t launch_linear(LinearParams p, const LinearPlan& plan, const CUtensorMap& tx, const CUtensorMap& tw,
                           cudaStream_t st);
 // Copies of up to two [rows][K] 16-bit operands (src null: none) into rows of K rounded up to 8 elements,

@@ -15,6 +15,12 @@
 //          x the BN), so the tile wastes no work on absent rows and W streams
 //          once.
 // Operands that TMA cannot address are copied to rows that it can first.
+//
+// The tensor cores' own fp32 sums lose a little at every addition (about half
+// a unit per 16 products, and always towards zero: 2e-6 of the result at K =
+// 3000), which a 16-bit output never shows.  For fp32 outputs the accumulator
+// is emptied every kFlushSteps K steps into fp32 registers that add with
+// rounding (FLUSH; two accumulators, so the products go on meanwhile).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,6 +37,8 @@ namespace {
 constexpr int BK = 64;                 // K per stage: one 128-byte swizzle row
 constexpr int kEpiThreads = 128;       // warps 0..3
 constexpr int kThreads = 192;          // + warp 4 (loads), warp 5 (MMA)
+
+constexpr int kFlushSteps = 8;         // 512 products
 
 struct __align__(8) TileBars {
   uint64_t full[8], empty[8];
@@ -341,12 +349,67 @@ __device__ __forceinline__ void tma_load_2d_pair(const CUtensorMap* map, uint64_
       : "memory");
 }
 
+// An epilogue warp's sums of the `parts` accumulators (two buffers of BN
+// columns from tl on; `before` of them were used before, both CTAs' epilogues
+// of a pair tell its leader), rounded to nearest in fp32 registers, written to
+// the columns at `out` for the epilogue.  The last buffer is not handed back.
+template <int BN, bool PAIR = false>
+__device__ __forceinline__ bool gather_parts(TileBars* bar, uint32_t tl, int parts, int before, uint32_t out,
+                                             const WaitCtl& ctl) {
+  constexpr int CH = BN < 32 ? BN : 32;
+  float sum[BN];
+#pragma unroll
+  for (int i = 0; i < BN; ++i) sum[i] = 0.f;
+#pragma unroll 1
+  for (int q = 0; q < parts; ++q) {
+    const int at = before + q, buf = at & 1;
+    if (!warp_wait(&bar->acc_full[buf], (at >> 1) & 1, ctl)) return false;
+    __syncwarp();
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < BN; c += CH) {
+      uint32_t r[32];
+      if constexpr (CH == 16) tmem_ld16(tl + buf * BN + c, r);
+      else tmem_ld32(tl + buf * BN + c, r);
+#pragma unroll
+      for (int i = 0; i < CH; ++i) sum[c + i] += __uint_as_float(r[i]);
+    }
+    if (q + 1 < parts) {
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) {
+        if constexpr (PAIR)
+          asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
+                       ::"r"(map_rank(smem_u32(&bar->acc_empty[buf]), 0)) : "memory");
+        else
+          mbar_arrive(&bar->acc_empty[buf]);
+      }
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < BN; c += CH) {
+    uint32_t r[32];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) r[i] = __float_as_uint(sum[c + i]);
+    if constexpr (CH == 16) {
+      uint32_t h[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) h[i] = r[i];
+      tmem_st16(out + c, h);
+    } else {
+      tmem_st32(out + c, r);
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- one-CTA tiles
 
 // SWAP: the MMA's 128 rows are W's and its BN columns x's.  DEEP: all of an
 // SM's shared memory for one CTA's stages, where there are no more CTAs than
 // SMs; otherwise half, so that two share an SM.
-template <int BN, bool SWAP, bool DEEP>
+template <int BN, bool SWAP, bool DEEP, bool FLUSH>
 struct TileCfg {
   static constexpr int STAGE = (128 + BN) * BK * 2;
   static constexpr int ST = DEEP ? (BN >= 128 ? 6 : 8) : (BN >= 128 ? 3 : (BN >= 64 ? 4 : 5));
@@ -355,7 +418,7 @@ struct TileCfg {
   static constexpr int DATA = PIPE;                     // behind RED, the epilogue's staging blocks
   static_assert(SWAP ? PIPE >= RED : PIPE >= RED + 4 * 32 * 33 * 4, "room for the epilogue");
   static constexpr int SMEM = DATA + BN * 4 + 512 + 1024;
-  static constexpr uint32_t TCOLS = BN < 32 ? 32u : static_cast<uint32_t>(BN);
+  static constexpr uint32_t TCOLS = FLUSH ? 2u * BN : (BN < 32 ? 32u : static_cast<uint32_t>(BN));
 };
 
 // Copies of operands whose rows TMA cannot address (row strides or addresses
@@ -413,11 +476,11 @@ __global__ void __launch_bounds__(256) repack_kernel(const RepackParams p) {
   }
 }
 
-template <int BN, bool SWAP, bool DEEP>
+template <int BN, bool SWAP, bool DEEP, bool FLUSH>
 __global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
 linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const LinearParams p) {
-  using C = TileCfg<BN, SWAP, DEEP>;
+  using C = TileCfg<BN, SWAP, DEEP, FLUSH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* sBias = reinterpret_cast<float*>(smem + C::DATA);
@@ -444,7 +507,10 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
       mbar_init(&bar->full[s], 1);
       mbar_init(&bar->empty[s], 1);
     }
-    mbar_init(&bar->acc_full[0], 1);
+    for (int i = 0; i < (FLUSH ? 2 : 1); ++i) {
+      mbar_init(&bar->acc_full[i], 1);
+      mbar_init(&bar->acc_empty[i], 4);                  // the epilogue warps
+    }
     bar->abort = 0;
     fence_mbarrier_init();
     // the first stages are free: their loads leave before the block meets
@@ -483,19 +549,25 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
     int s = 0;
     uint32_t par = 0;
     for (int k = kb; k < ke; ++k) {
+      const int in = FLUSH ? (k - kb) % kFlushSteps : k - kb, part = FLUSH ? (k - kb) / kFlushSteps : 0;
+      const uint32_t acc = tmem + (part & 1) * BN;
+      if (FLUSH && in == 0) {
+        if (part > 0) commit_if(lead, &bar->acc_full[(part - 1) & 1]);
+        if (!warp_wait(&bar->acc_empty[part & 1], ((part >> 1) & 1) ^ 1, ctl)) break;
+      }
       if (!warp_wait(&bar->full[s], par, ctl)) break;
       tc_fence_after();
       const uint32_t at = s * (C::STAGE / 16);
 #pragma unroll
       for (int kk = 0; kk < BK / 16; ++kk)
-        mma_f16_if<1>(lead, tmem, ad0 + at + kk * 2, bd0 + at + kk * 2, idesc, k > kb || kk > 0);
+        mma_f16_if<1>(lead, acc, ad0 + at + kk * 2, bd0 + at + kk * 2, idesc, in > 0 || kk > 0);
       commit_if(lead, &bar->empty[s]);
       if (++s == C::ST) {
         s = 0;
         par ^= 1;
       }
     }
-    commit_if(lead, &bar->acc_full[0]);
+    commit_if(lead, &bar->acc_full[FLUSH ? ((ke - kb - 1) / kFlushSteps) & 1 : 0]);
   } else {
     if (!SWAP) {
       for (int i = threadIdx.x; i < BN; i += kEpiThreads) {
@@ -511,7 +583,8 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
   const int row = (warp & 3) * 32 + lane;
   const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
   if (warp < 4) {
-    good = warp_wait(&bar->acc_full[0], 0, ctl);
+    if constexpr (FLUSH) good = gather_parts<BN>(bar, tl, (ke - kb + kFlushSteps - 1) / kFlushSteps, 0, tl, ctl);
+    else good = warp_wait(&bar->acc_full[0], 0, ctl);
     __syncwarp();
     tc_fence_after();
   }
@@ -627,27 +700,30 @@ linear_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constan
 
 // ---------------------------------------------------------------- pairs of CTAs
 
+template <int BN>
 struct PairCfg {
-  static constexpr int STAGE = (128 + 128) * BK * 2;     // per CTA: its rows of x, its rows of W
-  static constexpr int ST = 6;
-  static constexpr int BIAS = 4 * 256 * 4;               // each epilogue warp keeps its own copy
-  static constexpr int OUT = 4 * 32 * 33 * 4;           // and a staging block
+  static constexpr int STAGE = (128 + BN / 2) * BK * 2;  // per CTA: its rows of x, its rows of W
+  static constexpr int ST = BN == 256 ? 6 : 8;
+  static constexpr int BIAS = 4 * BN * 4;                // each epilogue warp keeps its own copy
+  static constexpr int OUT = 4 * 32 * 33 * 4;            // and a staging block
   static constexpr int SMEM = ST * STAGE + BIAS + OUT + 512 + 1024;
 };
 constexpr int kGroupM = 8;                               // tiles of x a column of W tiles is used for in a row
 
+// BN 256, or 128 with FLUSH (its sums are registers).
+template <int BN, bool FLUSH>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                    const LinearParams p) {
-  using C = PairCfg;
+  using C = PairCfg<BN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  float* sBias = reinterpret_cast<float*>(smem + C::ST * C::STAGE);   // [4][256]
+  float* sBias = reinterpret_cast<float*>(smem + C::ST * C::STAGE);   // [4][BN]
   TileBars* bar = reinterpret_cast<TileBars*>(smem + C::ST * C::STAGE + C::BIAS + C::OUT);
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  const int tiles_n = (p.N + 255) / 256;
+  const int tiles_n = (p.N + BN - 1) / BN;
   const long long n_tiles = static_cast<long long>(p.tiles_a) * tiles_n;
   const int n_pairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const int ksteps = (p.K + BK - 1) / BK;
@@ -699,7 +775,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
           if (leader) mbar_arrive_expect_tx(&bar->full[s], 2 * C::STAGE);
           uint8_t* dst = smem + s * C::STAGE;
           tma_load_2d_pair(&tmX, &bar->full[s], dst, k * BK, tm * 256 + static_cast<int>(rank) * 128);
-          tma_load_2d_pair(&tmW, &bar->full[s], dst + 128 * BK * 2, k * BK, tn * 256 + static_cast<int>(rank) * 128);
+          tma_load_2d_pair(&tmW, &bar->full[s], dst + 128 * BK * 2, k * BK, tn * BN + static_cast<int>(rank) * (BN / 2));
         }
       }
       // the last stages' commits have arrived before the CTA may exit
@@ -710,24 +786,26 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   } else if (warp == 5) {
     if (leader) {
       const uint32_t lead = elect_one() ? 1u : 0u;
-      const uint32_t idesc = instr_desc(p.in_bf16, p.in_bf16, 0, 256, 256);
+      const uint32_t idesc = instr_desc(p.in_bf16, p.in_bf16, 0, 256, BN);
       const uint64_t ad0 = smem_desc(smem_u32(smem), 16, 1024, 2u), bd0 = ad0 + 128 * BK * 2 / 16;
       int s = 0, n = 0;
       uint32_t par = 0;
       bool ok = true;
       for (long long t = pair; t < n_tiles && ok; t += n_pairs, ++n) {
-        const int buf = n & 1;
-        ok = warp_wait(&bar->acc_empty[buf], ((n >> 1) & 1) ^ 1, ctl);
-        if (!ok) break;
-        tc_fence_after();
         for (int k = 0; k < ksteps; ++k) {
+          const int in = FLUSH ? k % kFlushSteps : k;
+          if (in == 0) {
+            if (k > 0) commit_pair_if(lead, &bar->acc_full[(n++) & 1]);
+            ok = warp_wait(&bar->acc_empty[n & 1], ((n >> 1) & 1) ^ 1, ctl);
+            if (!ok) break;
+          }
           ok = warp_wait(&bar->full[s], par, ctl);
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = s * (C::STAGE / 16);
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk)
-            mma_f16_if<2>(lead, tmem + buf * 256u, ad0 + at + kk * 2, bd0 + at + kk * 2, idesc, k > 0 || kk > 0);
+            mma_f16_if<2>(lead, tmem + (n & 1) * BN, ad0 + at + kk * 2, bd0 + at + kk * 2, idesc, in > 0 || kk > 0);
           commit_pair_if(lead, &bar->empty[s]);
           if (++s == C::ST) {
             s = 0;
@@ -735,39 +813,44 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
           }
         }
         if (!ok) break;
-        commit_pair_if(lead, &bar->acc_full[buf]);
+        commit_pair_if(lead, &bar->acc_full[n & 1]);
       }
       if (!ok) settle();
     }
   } else {
     const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float* stage = reinterpret_cast<float*>(smem + C::ST * C::STAGE + C::BIAS) + warp * kStageFloats;
-    int n = 0;
-    for (long long t = pair; t < n_tiles; t += n_pairs, ++n) {
+    const int parts = FLUSH ? (ksteps + kFlushSteps - 1) / kFlushSteps : 1;
+    int n = 0;                                           // accumulators so far
+    for (long long t = pair; t < n_tiles; t += n_pairs, n += parts) {
       int tm, tn;
       place(t, tm, tn);
-      const int buf = n & 1;
+      const int buf = (n + parts - 1) & 1;
       // no barrier among the epilogue warps: one that gave up must not leave
       // the others waiting for it
-      float* bias = sBias + warp * 256;
+      float* bias = sBias + warp * BN;
       __syncwarp();
-      for (int i = lane; i < 256; i += 32) {
-        const int c = tn * 256 + i;
+      for (int i = lane; i < BN; i += 32) {
+        const int c = tn * BN + i;
         bias[i] = p.bias != nullptr && c < p.N ? load_as_f32(p.bias, c, p.bias_dtype) : 0.f;
       }
-      if (!warp_wait(&bar->acc_full[buf], (n >> 1) & 1, ctl)) break;
+      if constexpr (FLUSH) {
+        if (!gather_parts<BN, true>(bar, tl, parts, n, tl + buf * BN, ctl)) break;
+      } else {
+        if (!warp_wait(&bar->acc_full[buf], (n >> 1) & 1, ctl)) break;
+      }
       __syncwarp();
       tc_fence_after();
       const int64_t m0 = static_cast<int64_t>(tm) * 256 + rank * 128 + warp * 32;
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
+      for (int c = 0; c < BN; c += 32) {
         uint32_t r[32];
         __syncwarp();
-        tmem_ld32(tl + buf * 256 + c, r);
+        tmem_ld32(tl + buf * BN + c, r);
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-        if (tn * 256 + c < p.N) finish_rows(p, v, bias + c, m0, tn * 256 + c, stage);
+        if (tn * BN + c < p.N) finish_rows(p, v, bias + c, m0, tn * BN + c, stage);
       }
       tc_fence_before();
       __syncwarp();
@@ -785,10 +868,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constan
   }
 }
 
-template <int BN, bool SWAP, bool DEEP>
+template <int BN, bool SWAP, bool DEEP, bool FLUSH = false>
 cudaError_t launch_tile(const LinearParams& p, const CUtensorMap& ta, const CUtensorMap& tb, cudaStream_t st) {
-  using C = TileCfg<BN, SWAP, DEEP>;
-  auto kern = linear_tile_kernel<BN, SWAP, DEEP>;
+  using C = TileCfg<BN, SWAP, DEEP, FLUSH>;
+  auto kern = linear_tile_kernel<BN, SWAP, DEEP, FLUSH>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.tiles_a) * p.tiles_b * p.splits;
@@ -808,18 +891,36 @@ cudaError_t launch_tile(const LinearParams& p, const CUtensorMap& ta, const CUte
   return cudaLaunchKernelEx(&cfg, kern, ta, tb, p);
 }
 
+template <int BN, bool FLUSH>
+cudaError_t launch_pair(LinearParams p, const CUtensorMap& tx, const CUtensorMap& tw, cudaStream_t st) {
+  using C = PairCfg<BN>;
+  static_assert(C::SMEM <= 232448, "shared memory budget");
+  auto kern = linear_pair_kernel<BN, FLUSH>;
+  p.tiles_a = (p.M + 255) / 256;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const long long n_tiles = static_cast<long long>(p.tiles_a) * ((p.N + BN - 1) / BN);
+  const long long pairs = device_sm_count() / 2;
+  const int grid = static_cast<int>(2 * (n_tiles < pairs ? n_tiles : pairs));
+  kern<<<grid, kThreads, C::SMEM, st>>>(tx, tw, p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 // The kernel, tile and split of one problem: pure host arithmetic.
-LinearPlan plan_linear(int M, int N, int K) {
+LinearPlan plan_linear(int M, int N, int K, bool out_f32) {
   LinearPlan pl{};
-  const long long ksteps = (K + BK - 1) / BK;
-  const long long pair_tiles = static_cast<long long>((M + 255) / 256) * ((N + 255) / 256);
+  const long long ksteps = (static_cast<long long>(K) + BK - 1) / BK;
+  pl.flush = out_f32 && ksteps > kFlushSteps;
+  const int pn = pl.flush ? 128 : 256;
+  const long long pair_tiles = static_cast<long long>((M + 255) / 256) * ((N + pn - 1) / pn);
   // 256 x 256 tiles once they nearly fill the 74 pairs (1536 x 3000 x 1360, 72
   // tiles: 17.6 us against 19.1; 1024 x 4096 x 1024, 64 tiles: 12.6 against
   // 11.8)
   if (pair_tiles >= 68) {
     pl.pair = true;
+    pl.bn = pn;
     return pl;
   }
   pl.splits = 1;
@@ -869,22 +970,17 @@ cudaError_t launch_linear(LinearParams p, const LinearPlan& pl, const CUtensorMa
                           cudaStream_t st) {
   p.vec_y = vector_bytes(p.y, p.ldy, p.out_dtype);
   p.vec_r = p.residual != nullptr ? vector_bytes(p.residual, p.ldr, p.out_dtype) : 0;
-  if (pl.pair) {
-    p.tiles_a = (p.M + 255) / 256;
-    cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::SMEM);
-    if (e != cudaSuccess) return e;
-    const long long n_tiles = static_cast<long long>(p.tiles_a) * ((p.N + 255) / 256);
-    const long long pairs = device_sm_count() / 2;
-    const int grid = static_cast<int>(2 * (n_tiles < pairs ? n_tiles : pairs));
-    linear_pair_kernel<<<grid, kThreads, PairCfg::SMEM, st>>>(tx, tw, p);
-    return cudaGetLastError();
-  }
+  if (pl.pair) return pl.flush ? launch_pair<128, true>(p, tx, tw, st) : launch_pair<256, false>(p, tx, tw, st);
   p.splits = pl.splits;
   const int rows_a = pl.swap ? p.N : p.M, rows_b = pl.swap ? p.M : p.N;
   p.tiles_a = (rows_a + 127) / 128;
   p.tiles_b = (rows_b + pl.bn - 1) / pl.bn;
   const CUtensorMap& ta = pl.swap ? tw : tx;
   const CUtensorMap& tb = pl.swap ? tx : tw;
+  if (pl.flush) {
+    if (pl.swap) return pl.bn == 16 ? launch_tile<16, true, false, true>(p, ta, tb, st) : launch_tile<32, true, false, true>(p, ta, tb, st);
+    return pl.bn == 64 ? launch_tile<64, false, false, true>(p, ta, tb, st) : launch_tile<128, false, false, true>(p, ta, tb, st);
+  }
   if (static_cast<long long>(p.tiles_a) * p.tiles_b * p.splits <= device_sm_count()) {
     if (pl.swap) return pl.bn == 16 ? launch_tile<16, true, true>(p, ta, tb, st) : launch_tile<32, true, true>(p, ta, tb, st);
     return pl.bn == 64 ? launch_tile<64, false, true>(p, ta, tb, st) : launch_tile<128, false, true>(p, ta, tb, st);

@@ -128,6 +128,17 @@ def test_activations_at_the_ends(cuda_device, out):
         assert ((got[fine] - want[fine]).abs() <= tol).all(), (act, got[:, 0], want[:, 0])
 
 
+@pytest.mark.parametrize("M,N,K", [(5, 300, 8192), (30, 130, 5000), (150, 300, 8192), (1000, 1300, 4100), (2304, 4480, 4096)])
+def test_long_sums_in_fp32(cuda_device, M, N, K):
+    """An fp32 output of a long sum: runs of 512 products, in which the tensor
+    cores make 32 additions that each lose at most 2^-23 of the sum, half of
+    it on average -- 32 * 2^-24 of the result -- and rounded sums of the runs."""
+    x, w, _, _ = make(cuda_device, "bf16", M, N, K, seed=K)
+    y = jattn.linear(x, w, out_dtype=torch.float32).double()
+    want = x.double() @ w.double().t()
+    assert (y - want).norm() <= 2.0 ** -19 * want.norm()
+
+
 def test_same_bits_every_time(cuda_device):
     for M, N, K in ((4, 512, 4096), (100, 256, 2048), (2500, 2700, 264)):
         x, w, b, _ = make(cuda_device, "fp16", M, N, K)
