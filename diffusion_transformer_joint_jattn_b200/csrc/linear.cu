@@ -917,8 +917,9 @@ LinearPlan plan_linear(int M, int N, int K, bool out_f32) {
   const long long pair_tiles = static_cast<long long>((M + 255) / 256) * ((N + pn - 1) / pn);
   // 256 x 256 tiles once they nearly fill the 74 pairs (1536 x 3000 x 1360, 72
   // tiles: 17.6 us against 19.1; 1024 x 4096 x 1024, 64 tiles: 12.6 against
-  // 11.8)
-  if (pair_tiles >= 68) {
+  // 11.8); emptying their accumulators on the way they need several rounds
+  // (2048 x 2048 x 2048 to fp32, 128 tiles: 40 us against 29)
+  if (pair_tiles >= (pl.flush ? 296 : 68)) {
     pl.pair = true;
     pl.bn = pn;
     return pl;
@@ -942,8 +943,12 @@ LinearPlan plan_linear(int M, int N, int K, bool out_f32) {
   // of them would idle (768 x 768 x 3000, 72 tiles: 13.7 us in halves, 17.3
   // whole, 20.9 in quarters; 1024 x 1024 x 1024, 128 tiles: 6.6 whole, 9.8 in
   // halves), otherwise 128 (512 x 4096 x 4096: 19.4 us with 128, 23.9 with 64)
+  // -- unless two 64-column tiles fit on an SM and the epilogue, half as long
+  // for them, weighs as much as the products: short sums (1000 x 1500 x 400
+  // with gelu: 14.1 us, with 128 columns 19.9) and gathered ones (1531 x 777 x
+  // 1003 to fp32 with silu: 21.7 and 31.7)
   const long long tiles = static_cast<long long>((M + 127) / 128) * ((N + 63) / 64);
-  pl.bn = tiles <= 148 ? 64 : 128;
+  pl.bn = tiles <= 148 || (tiles <= 296 && (pl.flush || ksteps < 16)) ? 64 : 128;
   while (pl.splits < 4 && tiles * pl.splits * 2 <= 148 && ksteps / (pl.splits * 2) >= 4) pl.splits *= 2;
   return pl;
 }
