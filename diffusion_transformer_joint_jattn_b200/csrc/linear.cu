@@ -185,13 +185,35 @@ __device__ __forceinline__ void finish_rows(const LinearParams& p, float (&v)[W]
 #pragma unroll
     for (int i = 0; i < W; ++i) stage[lane * (W + 1) + i] = v[i];
     __syncwarp();
-    const int c = lane % W, n_at = n + c;
-#pragma unroll 4
-    for (int r = lane / W; r < 32; r += 32 / W) {
-      if (m0 + r >= p.M || n_at >= p.N) continue;
-      float x = stage[r * (W + 1) + c];
-      if (p.residual != nullptr) x += load_as_f32(p.residual, (m0 + r) * p.ldr + n_at, p.out_dtype);
-      store_from_f32(p.y, (m0 + r) * p.ldy + n_at, p.out_dtype, x);
+    // column n + c of the rows r0, r0 + 32 / W, ...: every residual element on
+    // its way before the first is used (clamped addresses: no branch between)
+    constexpr int ROUNDS = W;
+    const int c = lane % W, r0 = lane / W;
+    const bool in = n + c < p.N;
+    const int64_t n_at = min(n + c, p.N - 1);
+    float x[ROUNDS];
+    if (p.residual != nullptr) {
+      const int64_t last = p.M - 1;
+      if (f32) {
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k)
+          x[k] = static_cast<const float*>(p.residual)[min(m0 + r0 + k * (32 / W), last) * p.ldr + n_at];
+      } else {
+        uint16_t h[ROUNDS];
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k)
+          h[k] = static_cast<const uint16_t*>(p.residual)[min(m0 + r0 + k * (32 / W), last) * p.ldr + n_at];
+#pragma unroll
+        for (int k = 0; k < ROUNDS; ++k) x[k] = widen16(h[k], bf16);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < ROUNDS; ++k) x[k] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < ROUNDS; ++k) {
+      const int r = r0 + k * (32 / W);
+      if (in && m0 + r < p.M) store_from_f32(p.y, (m0 + r) * p.ldy + n_at, p.out_dtype, x[k] + stage[r * (W + 1) + c]);
     }
     return;
   }

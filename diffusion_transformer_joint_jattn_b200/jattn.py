@@ -857,7 +857,7 @@ def linear(x, w, bias=None, act: str = "none", residual=None, out=None, out_dtyp
         ldr = N if residual.is_contiguous() else _rows(residual, "residual")
     ldy = N
     if out is None:
-        out = x.new_empty(shape, dtype=out_dtype)
+        out = x.new_empty(*shape, dtype=out_dtype)
     else:
         _float_check(out, "out", dev, (out_dtype,))
         if out.shape != shape:
@@ -947,13 +947,13 @@ def fwd_diff(q, k, v, lam, lambda_init: float, norm_w=None, eps: float = 1e-5, k
         _plain_check(key_mask, "key_mask", dev, _MASKS, (B, S_kv))
         mask_ptr = key_mask.data_ptr()
     if o is None:
-        o = q.new_empty((B, S_q, H, d), dtype=torch.bfloat16)
+        o = q.new_empty(B, S_q, H, d, dtype=torch.bfloat16)
     else:
         _plain_check(o, "o", dev, _BF16, (B, S_q, H, d))
     if lse is not None:
         _plain_check(lse, "lse", dev, _F32, (2, B, H, S_q))
     elif want_lse:
-        lse = q.new_empty((2, B, H, S_q), dtype=torch.float32)
+        lse = q.new_empty(2, B, H, S_q, dtype=torch.float32)
     if lse is not None:
         lse_ptr = lse.data_ptr()
     sh = _DIFF_SHAPE.pack(B, H, H_kv, S_q, S_kv, d, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0], vs[1], vs[2])
