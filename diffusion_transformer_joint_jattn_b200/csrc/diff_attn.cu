@@ -863,10 +863,13 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             tmem_ld32(to + c, o);
             if (live) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(dst + c + e) =
-                    make_float4(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                                __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)           // whole 32-byte sectors of the thread's row
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                             ::"l"(dst + c + e), "r"(o[e]), "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]),
+                               "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
+                             : "memory");
             }
           }
           if (live && !(QUAD && lo_role)) p.part_l[(slot * 2 + t) * BM + row] = lse2;
