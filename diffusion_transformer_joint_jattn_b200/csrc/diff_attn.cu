@@ -1254,9 +1254,15 @@ DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms) {
   return w;
 }
 
-// Whether bf16 operands get an fp16 copy of V: worth its three passes over V
-// once several row tiles walk each V tile.
-bool diff_widens_v(int n_rt) { return n_rt >= 4; }
+// Whether bf16 operands get an fp16 copy of V: about 8 us and three passes over
+// V, against a fifth of the walk for P in two parts.  Several row tiles have to
+// share each V tile, and the walk to be long: 2 x 24 heads, 1000 tokens (20 key
+// tiles per SM): 75 us with the copy, 77 without; 2 x 24 x 4608: 941 and 1169;
+// 8 heads, 2000 tokens (14): 85 and 83; 24 heads, 300 x 8000 (3 row tiles):
+// 127 and 112.
+bool diff_widens_v(long long items, int n_rt, int S_kv, int sms) {
+  return n_rt >= 4 && items * ((S_kv + BN - 1) / BN) >= 18ll * sms;
+}
 
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st) {

@@ -231,7 +231,7 @@ struct DiffWalk {
   int ctas, merge;
 };
 DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms);
-bool diff_widens_v(int n_rt);
+bool diff_widens_v(long long items, int n_rt, int S_kv, int sms);
 // Ranges of at most this many rows are walked by a kernel of their own.
 constexpr int kQuadRows = 32;
 // The maps describe (d, rows, heads or ranges, batch) with boxes of 64 x 128 (q's: 64 x 32 where R <= kQuadRows).

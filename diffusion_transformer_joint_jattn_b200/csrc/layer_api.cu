@@ -48,6 +48,7 @@ struct DiffRanges {
   int n_groups, hpg, R, n_rt;
   int64_t items;
   jattn::DiffWalk walk;
+  bool widen;                   // with bf16 operands
   int64_t row_stride, group_stride;
 };
 
@@ -74,7 +75,9 @@ jattn_status diff_ranges(const jattn_diff_shape* s, DiffRanges* r) {
   r->row_stride = s->S_q == 1 ? s->q_stride[1] : s->q_stride[2];
   r->group_stride = r->hpg * s->q_stride[1];
   r->items = static_cast<int64_t>(s->B) * r->n_groups * r->n_rt;
-  r->walk = jattn::diff_walk(r->items, r->n_rt, s->S_kv, jattn::device_sm_count());
+  const int sms = jattn::device_sm_count();
+  r->walk = jattn::diff_walk(r->items, r->n_rt, s->S_kv, sms);
+  r->widen = jattn::diff_widens_v(r->items, r->n_rt, s->S_kv, sms);
   return JATTN_OK;
 }
 
@@ -92,7 +95,7 @@ DiffLayout diff_layout(const jattn_diff_shape* s, const DiffRanges& r, bool in_b
     L.part_o = seg(static_cast<size_t>(r.walk.ctas) * 4 * 128 * s->d * 4);
     L.part_l = seg(static_cast<size_t>(r.walk.ctas) * 4 * 128 * 4);
   }
-  if (in_bf16 && jattn::diff_widens_v(r.n_rt) && s->S_kv > 0) {
+  if (in_bf16 && r.widen) {
     L.v16 = seg(static_cast<size_t>(s->B) * s->H_kv * s->S_kv * s->d * 2);
     L.v_amax = seg(static_cast<size_t>(s->B) * s->H_kv * 4);
   }
@@ -317,7 +320,7 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
     p.part_o = reinterpret_cast<float*>(ws + L.part_o);
     p.part_l = reinterpret_cast<float*>(ws + L.part_l);
   }
-  const bool widen = in_bf16 && jattn::diff_widens_v(r.n_rt) && s->S_kv > 0;
+  const bool widen = in_bf16 && r.widen;
   if (widen) {
     p.v = static_cast<const __nv_bfloat16*>(v);
     for (int i = 0; i < 3; ++i) p.v_stride[i] = s->v_stride[i];

@@ -113,6 +113,40 @@ def test_key_mask(cuda_device, S_q, bad):
         assert (o[3] == 0).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_walk(cuda_device, d):
+    """Whole waves of items and a shared tail, bf16 V copied to fp16 with a power
+    of two per head (here 2^-40 to 2^40, and a head of zeros), lengths and mask
+    together; against the oracle on some of the heads."""
+    B, H, S = 2, 24, 1050
+    q, k, v, lam, w = make(cuda_device, "bf16", B, H, H, S, S, d, seed=11)
+    e = torch.arange(B * H, device=cuda_device).view(B, H, 1, 1)
+    v.mul_(torch.pow(2.0, (e % 9 - 4) * 10.0))
+    v[1, 3] = 0
+    lens = np.array([S, 700])
+    allowed = np.random.default_rng(1).random((B, S)) < 0.9
+    m = torch.from_numpy(allowed).to(cuda_device)
+    v[0].masked_fill_(~m[0][None, :, None], float("nan"))
+    allowed &= np.arange(S)[None] < lens[:, None]
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    for norm in (None, w):
+        o, lse = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=norm, eps=EPS, kv_len=n, key_mask=m, want_lse=True)
+        for h in (0, 3, 4, 8, 13, 23):
+            vh = torch.nan_to_num(v[:, h:h + 1])
+            if norm is None:
+                # a power of two out of V is one out of O: held in the units of N(0, 1) values
+                f = torch.pow(2.0, -(e[:, h:h + 1] % 9 - 4) * 10.0)
+                check(o[:, :, h:h + 1].double() * f.transpose(1, 2), lse[:, :, h:h + 1], q[:, h:h + 1], k[:, h:h + 1],
+                      vh.double() * f, lam[:, h:h + 1], norm, allowed)
+            else:
+                big = (e[:, h] % 9 - 4 >= 0).view(B)     # eps hides what is far below 1
+                for b in range(B):
+                    if big[b] or (b == 1 and h == 3):
+                        s = slice(b, b + 1)
+                        check(o[s, :, h:h + 1], lse[:, s, h:h + 1], q[s, h:h + 1], k[s, h:h + 1], vh[s], lam[:, h:h + 1],
+                              norm, allowed[s])
+
+
 def test_split_and_whole_walk_agree(cuda_device):
     """The same queries alone (keys split over CTAs) and among enough others to
     fill the GPU (one walk): within both forms' rounding of the output."""

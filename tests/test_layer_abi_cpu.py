@@ -118,7 +118,8 @@ def test_diff_workspace():
     assert size(1, 4, 2, 3, 9) == 0                                  # short: one walk, P in two parts
     assert size(1, 4, 2, 3, 9, d=96) == 0 and size(1, 3, 2, 3, 9) == 0
     assert size(1, 2, 2, 300, 300, dt=jattn.FP16) == 0
-    assert size(1, 2, 2, 512, 300) >= 2 * 300 * 128 * 2              # bf16, several row tiles: V in fp16
+    # bf16, several row tiles and a long walk: V in fp16 too
+    assert size(2, 24, 24, 1024, 1024) - size(2, 24, 24, 1024, 1024, dt=jattn.FP16) >= 48 * 1024 * 128 * 2
     # one query over a long cache: parts of up to 148 CTAs, and no copy of V
     n = size(1, 8, 8, 1, 16384)
     assert 0 < n <= 148 * 4 * 128 * 129 * 4 + 1024
