@@ -132,3 +132,78 @@ def test_joint_attention_output_projection(cuda_device, path):
     y3 = jattn.joint_attention(*args, proj_w=wo, proj_b=bo, residual=x, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y3, y)
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """Elements more than 2^32 from their tensor's start: the last sequence of a
+    cache of 5.4e9 elements (what is not its keys is never read), a rotary
+    view and the rows of a linear layer with strides of 2^31 elements."""
+    B, n, cap, d, L = 5, 8, 1 << 20, 128, 300
+    g = torch.Generator().manual_seed(5)
+    mk = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda_device)  # noqa: E731
+    k, v = (torch.empty(B, n, cap, d, dtype=torch.bfloat16, device=cuda_device) for _ in range(2))
+    assert k.numel() > 1 << 32
+    q, ks, vs, lam = mk(B, n, 1, d), mk(1, n, L, d), mk(1, n, L, d), 0.1 * torch.randn(4, n, d // 2, generator=g)
+    k[-1:, :, :L], v[-1:, :, :L] = ks, vs
+    lens = torch.tensor([0, 0, 0, 0, L], dtype=torch.int32, device=cuda_device)
+    o, _ = jattn.fwd_diff(q, k, v, lam.to(cuda_device), INIT, kv_len=lens)
+    want, _ = jattn.fwd_diff(q[-1:], ks, vs, lam.to(cuda_device), INIT)
+    # the same keys in other shares of the walk: both forms' rounding
+    assert torch.allclose(o[-1:].float(), want.float(), rtol=2 * 2.0 ** -8, atol=2.0 ** -9) and (o[:-1] == 0).all()
+    freqs, _ = jattn.rotary_freqs(d, device=cuda_device)
+    pos = torch.arange(2, device=cuda_device).int()
+    far = k[:, 3:5, 77].view(B, 1, 2, d)[-2:].expand(2, 1, 2, d)          # strides of n * cap * d elements
+    far.copy_(mk(2, 1, 2, d))
+    near = far.contiguous()
+    pos1 = pos[1:].contiguous()
+    assert torch.equal(jattn.rotary(far, None, pos1, freqs)[0], jattn.rotary(near, None, pos1, freqs)[0])
+    jattn.rotary(far, None, pos1, freqs, out=(far,))
+    assert torch.equal(far, jattn.rotary(near, None, pos1, freqs)[0])
+    flat = k.view(-1)
+    K, N, step = 64, 96, 1 << 31
+    w = mk(N, K)
+    for off in (0, 1):                                                    # addressed by TMA, and copied first
+        x = flat[off:].as_strided((3, K), (step, 1), storage_offset=off)
+        x.copy_(mk(3, K))
+        y = v.view(-1).as_strided((3, N), (step, 1), storage_offset=off)
+        assert torch.equal(jattn.linear(x, w, out=y), jattn.linear(x.contiguous(), w))
+    assert jattn.device_status()[0] == jattn.OK
+
+
+def test_two_streams_at_once(cuda_device):
+    """Calls on two streams share nothing: the results are those of one."""
+    g = torch.Generator().manual_seed(6)
+    mk = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda_device)  # noqa: E731
+    q, k, v = mk(1, 8, 1, 128), mk(1, 2, 6000, 128), mk(1, 2, 6000, 128)
+    lam = (0.1 * torch.randn(4, 8, 64, generator=g)).to(cuda_device)
+    x, w = mk(40, 1003), mk(777, 1003)
+    want_o, want_y = jattn.fwd_diff(q, k, v, lam, INIT)[0], jattn.linear(x, w)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[] for _ in streams]
+    for _ in range(20):
+        for s, out in zip(streams, got):
+            out.append((jattn.fwd_diff(q, k, v, lam, INIT, stream=s)[0], jattn.linear(x, w, stream=s)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want_o) and torch.equal(y, want_y) for out in got for o, y in out)
+
+
+def test_workspaces_of_the_caller(cuda_device):
+    """A workspace given is used (and big enough at the size asked for)."""
+    g = torch.Generator().manual_seed(7)
+    mk = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16).to(cuda_device)  # noqa: E731
+    q, k, v = mk(1, 4, 1, 64), mk(1, 4, 3000, 64), mk(1, 4, 3000, 64)
+    lam = (0.1 * torch.randn(4, 4, 32, generator=g)).to(cuda_device)
+    x, w = mk(10, 33), mk(20, 33)
+    lib = jattn.load()
+    need = lib.jattn_fwd_diff_workspace(jattn._DIFF_SHAPE.pack(1, 4, 4, 1, 3000, 64, *q.stride()[:3], *k.stride()[:3],
+                                                               *v.stride()[:3]), jattn.BF16)
+    need_y = lib.jattn_linear_workspace(jattn._LINEAR_SHAPE.pack(10, 20, 33, 33, 33, 20, 20, 0, 0, 0, 0), x.data_ptr(),
+                                        w.data_ptr())
+    assert need > 0 and need_y == 1024 + 1792
+    for n, f in ((need, lambda ws: jattn.fwd_diff(q, k, v, lam, INIT, workspace=ws)[0]),
+                 (need_y, lambda ws: jattn.linear(x, w, workspace=ws))):
+        ws = torch.full((n + 512,), 77, dtype=torch.uint8, device=cuda_device)
+        assert torch.equal(f(ws[:n]), f(None)) and (ws[n:] == 77).all() and not (ws[:n] == 77).all()
+        with pytest.raises(ValueError):
+            f(ws[:n - 1])
