@@ -70,7 +70,7 @@ jattn_status diff_ranges(const jattn_diff_shape* s, DiffRanges* r) {
   r->hpg = packed ? G : 1;
   const int64_t rows = static_cast<int64_t>(r->hpg) * s->S_q;
   r->n_rt = static_cast<int>((rows + 127) / 128);
-  if (rows > INT32_MAX || static_cast<int64_t>(s->B) * r->n_groups * r->n_rt > INT32_MAX) return JATTN_ERR_INVALID_ARG;
+  if (rows > (1 << 30) || static_cast<int64_t>(s->B) * r->n_groups * r->n_rt > (1 << 30)) return JATTN_ERR_INVALID_ARG;
   r->R = static_cast<int>(rows);
   r->row_stride = s->S_q == 1 ? s->q_stride[1] : s->q_stride[2];
   r->group_stride = r->hpg * s->q_stride[1];
@@ -215,7 +215,7 @@ jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void
   if (bias != nullptr && !is_float(s->bias_dtype)) return JATTN_ERR_UNSUPPORTED;
   if (s->act < JATTN_ACT_NONE || s->act > JATTN_ACT_RELU) return JATTN_ERR_UNSUPPORTED;
   if (s->M == 0 || s->N == 0) return JATTN_OK;
-  if (x == nullptr || w == nullptr || y == nullptr) return JATTN_ERR_INVALID_ARG;
+  if (x == nullptr || w == nullptr || y == nullptr || y == x || y == w) return JATTN_ERR_INVALID_ARG;
   const int64_t most = int64_t{1} << 38;
   if (s->ldx < s->K || s->ldw < s->K || s->ldy < s->N || s->ldx >= most || s->ldw >= most || s->ldy >= most)
     return JATTN_ERR_INVALID_ARG;

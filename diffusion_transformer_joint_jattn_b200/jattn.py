@@ -670,6 +670,8 @@ def _workspace_check(t, dev: int, need: int):
         raise ValueError(f"workspace must hold at least {need} contiguous bytes, got {t.numel()}")
 
 
+# The current stream and device by torch's own C functions: a Stream object per
+# call costs 3 us, a quarter of a small call.
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _MASKS = (torch.bool, torch.uint8)
 

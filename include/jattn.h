@@ -431,7 +431,8 @@ typedef struct {
  * Linear layer with its epilogue: y = act(x w^T + bias) + residual, sums and
  * epilogue in fp32, one rounding.
  *   x [M][K], w [N][K] : in_dtype;  bias [N] or NULL;  residual [M][N] or
- *   NULL (may be y itself, with ldr == ldy; y overlaps nothing else).
+ *   NULL (may be y itself, with ldr == ldy; y overlaps nothing else, x and w
+ *   included).
  * Any sizes and strides.  An x or w whose address or row stride is not a
  * multiple of 16 bytes is first copied into the workspace: device scratch of
  * at least jattn_linear_workspace(shape, x, w) bytes, 256-byte aligned (NULL
@@ -449,7 +450,7 @@ jattn_status jattn_linear(const jattn_linear_shape* shape, const void* x, const 
 /* Differential attention's shape.  Strides in elements over (batch entry,
  * head, token), multiples of 8; channels contiguous.  d in {64, 128};
  * H_kv >= 1 divides H; B, S_q, S_kv >= 0 (S_kv 0: every row is empty),
- * S_q, S_kv <= 2^24, B * H <= 65535. */
+ * S_q, S_kv <= 2^24, B * H <= 65535, (H / H_kv) * S_q <= 2^30. */
 typedef struct {
   int32_t B, H, H_kv, S_q, S_kv, d;
   int64_t q_stride[3], k_stride[3], v_stride[3];

@@ -42,7 +42,7 @@ def test_rotary_without_work_is_ok():
 
 def linear(code, **kw):
     a = dict(dict(M=4, N=8, K=16, ldx=16, ldw=16, ldy=8, ldr=8, i=jattn.BF16, o=jattn.BF16, b=jattn.BF16, act=0, x=A, w=A,
-                  bias=None, res=None, y=A, ws=None, n=0), **kw)
+                  bias=None, res=None, y=2 * A, ws=None, n=0), **kw)
     sh = jattn._LINEAR_SHAPE.pack(a["M"], a["N"], a["K"], a["ldx"], a["ldw"], a["ldy"], a["ldr"], a["i"], a["o"], a["b"],
                                   a["act"])
     got = jattn.load().jattn_linear(sh, a["x"], a["w"], a["bias"], a["res"], a["y"], a["ws"], a["n"], None)
@@ -51,7 +51,7 @@ def linear(code, **kw):
 
 def test_linear_refusals():
     for kw in (dict(M=-1), dict(N=-1), dict(K=0), dict(ldx=15), dict(ldw=8), dict(ldy=7), dict(res=A, ldr=7), dict(x=None),
-               dict(w=None), dict(y=None), dict(res=A, y=A, ldy=16), dict(ldx=1 << 38),
+               dict(w=None), dict(y=None), dict(res=2 * A, ldy=16), dict(y=A), dict(ldx=1 << 38),
                dict(M=(1 << 30) + 1), dict(N=(1 << 30) + 1, ldy=1 << 31), dict(K=(1 << 30) + 1, ldx=1 << 31, ldw=1 << 31)):
         linear(INV, **kw)
     for kw in (dict(i=jattn.FP32), dict(i=jattn.E4M3), dict(o=jattn.E4M3), dict(bias=A, b=jattn.E4M3), dict(act=5), dict(act=-1)):
