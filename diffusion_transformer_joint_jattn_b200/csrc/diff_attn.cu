@@ -833,7 +833,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if constexpr (!QUAD) arrive_if(lane == 0, &bar->turn[t ^ 1][warp & 3]);
         tmem_wait_st();
         l_run += (acc0.x + acc0.y) + (acc1.x + acc1.y);
-        if (mx != mx) l_run = mx;                       // NaN in, NaN out
+        // NaN in, NaN out, and so for a logit of +inf
+        if (!(mx < INFINITY)) l_run = __int_as_float(0x7FFFFFFF);
         // one arrival per warp: 128 to one address take turns
         tc_fence_before();
         __syncwarp();
@@ -1056,14 +1057,17 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   const long long total = shared_prefix(p, p.B);
   const Runs runs(total, ctas);
   const long long g = runs.start(cta);
-  if (g >= total) return;
-  long long item;
-  int off;
-  locate(p, g, item, off);
-  if (off == 0 || runs.start(cta - 1) > g - off) return;
+  long long item = 0;
+  int off = 0;
+  if (g < total) locate(p, g, item, off);
+  const bool first = off > 0 && runs.start(cta - 1) <= g - off;
   const int range = static_cast<int>(divide(item, p.n_rt)), b = range / p.n_groups, gi = range % p.n_groups;
   const int r = static_cast<int>(item - static_cast<long long>(range) * p.n_rt) * BM + row;
-  if (r >= p.R) return;                                 // WPR 4: the whole block
+  // Everything above is the inputs' alone; the parts from here on.  Every block
+  // waits for the walk, also one without work: this grid's end has to mean the
+  // walk's end for what the stream holds next.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!first || r >= p.R) return;                       // WPR 4: the whole block
   // the last CTA that has a part of the item, by its last tile
   const int parts = runs.owner(g - off + tiles_of(p, b) - 1) - cta + 2;
   const int head = gi * p.hpg + r / p.S_q, s_q = r % p.S_q;
@@ -1074,8 +1078,6 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
     const size_t slot = i == 0 ? 2 * static_cast<size_t>(cta - 1) + 1 : 2 * static_cast<size_t>(cta + i - 1);
     return (slot * 2 + t) * BM + row;
   };
-  // everything above is the inputs' alone: the parts from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int t = 0; t < 2; ++t) {

@@ -188,6 +188,28 @@ def test_large_logits_and_scale(cuda_device):
     assert np.linalg.norm(f(o) - want) <= (2.0 ** -8 + 2.0 ** -5) * np.linalg.norm(want)
 
 
+def test_nan_and_infinite_logits_stay_in_their_rows(cuda_device):
+    """A query of NaN, one whose logit with some key is +inf, in every column of a
+    key half (some exponentials are computed another way): NaN in that row's
+    output and log-sum-exp, the other rows as they were."""
+    for S_q in (3, 70):
+        q, k, v, lam, w = make(cuda_device, "fp16", 1, 1, 1, S_q, 64, 128)
+        clean, lse = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, want_lse=True)
+        for col in range(64):
+            q2, k2 = q.clone(), k.clone()
+            q2[0, 0, 0, 5] = float("nan")
+            k2[0, 0, col, 70] = float("inf")              # map 2: +inf where q's channel is positive
+            q2[0, 0, 1, 70], q2[0, 0, 2:, 70] = 1.0, 0.0
+            k3 = k2.clone()
+            k3[0, 0, col, 70] = 0.0
+            o, l = jattn.fwd_diff(q2, k2, v, lam, INIT, norm_w=w, want_lse=True)
+            assert torch.isnan(o[0, 0]).all() and torch.isnan(o[0, 1]).all() and torch.isnan(l[0, 0, 0, 0])
+            assert torch.isnan(l[1, 0, 0, 1])
+            o3, _ = jattn.fwd_diff(q2, k3, v, lam, INIT, norm_w=w)
+            assert torch.isfinite(o3[0, 1:]).all()
+        assert torch.isfinite(clean).all()
+
+
 def test_no_keys_and_no_queries(cuda_device):
     q, k, v, lam, w = make(cuda_device, "bf16", 2, 2, 1, 3, 4, 64)
     o, lse = jattn.fwd_diff(q, k[:, :, :0], v[:, :, :0], lam, INIT, norm_w=w, want_lse=True)
