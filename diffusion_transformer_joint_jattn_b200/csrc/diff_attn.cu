@@ -447,14 +447,14 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bar->q_full, 1);
-    mbar_init(&bar->q_empty, 1);
+    mbar_init(&bar->q_empty, 2);
     for (int s = 0; s < C::KS; ++s) {
       mbar_init(&bar->k_full[s], 1);
-      mbar_init(&bar->k_empty[s], 1);
+      mbar_init(&bar->k_empty[s], 2);
     }
     for (int s = 0; s < C::VS; ++s) {
       mbar_init(&bar->v_full[s], 1);
-      mbar_init(&bar->v_empty[s], 1);
+      mbar_init(&bar->v_empty[s], 2);
       mbar_init(&bar->v_ready[s], 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -554,7 +554,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int nv = nk - (v_behind ? 1 : 0);
         for (int i = max(nv - C::VS, 0); i < nv; ++i) drain_wait(&bar->v_full[i % C::VS], (i / C::VS) & 1, ctl);
       }
-    } else if (warp == kMmaWarp) {
+    } else if (warp == kMmaWarp || warp == kShareWarp) {
+      const int t = warp == kMmaWarp ? 0 : 1;         // the map whose products this warp issues
       // The whole warp walks, one lane issues: the descriptors are then warp
       // uniform and live in uniform registers.  With one lane walking, each
       // MMA cost 72 clocks to issue (measured; its execution 48 or 64).
@@ -567,8 +568,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       // constant: the issuing thread's instructions are on the S -> P chain.
       const uint64_t qd0 = smem_desc(sQa, 16, 1024, 2u), kd0 = smem_desc(sKa, 16, 1024, 2u);
       const uint64_t vd0 = smem_desc(sVa, C::BOXB, 1024, 2u);
-      // S of map t, keys [64 half, +64) of the K tile in stage ks
-      auto issue_qk = [&](int t, int ks, int half, int buf) {
+      // S of the map, keys [64 half, +64) of the K tile in stage ks
+      auto issue_qk = [&](int ks, int half, int buf) {
         const uint64_t kd = kd0 + static_cast<uint32_t>(ks * (C::TB / 16) + half * (64 * 128 / 16));
 #pragma unroll
         for (int kk = 0; kk < DM / 16; ++kk) {
@@ -577,7 +578,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           mma_ss_if(lead, tmem + col_s(t, buf), qd0 + off, kd + off, idesc_qk, kk > 0);
         }
       };
-      auto issue_pv = [&](int t, int vs, int half, int buf, bool acc) {
+      auto issue_pv = [&](int vs, int half, int buf, bool acc) {
         const uint64_t vd = vd0 + static_cast<uint32_t>(vs * (C::TB / 16) + half * (64 * 128 / 16));
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
@@ -604,11 +605,8 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // half, so that S commit n + 1 proves the last P.V done.
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (i < n) issue_qk(t, nk % C::KS, i, (idx + i) & 1);
-            commit_if(lead, &bar->s_full[t][(idx + i) & 1]);
-          }
+          if (i < n) issue_qk(nk % C::KS, i, (idx + i) & 1);
+          commit_if(lead, &bar->s_full[t][(idx + i) & 1]);
         }
         commit_if(lead, &bar->k_empty[nk % C::KS]);
         ++nk;
@@ -624,16 +622,12 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                  (!more || warp_wait(&bar->k_full[ks], k_par, ctl));
             if (!ok) break;
           }
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            ok = warp_wait(&bar->p_full[t][buf], (p_phase >> buf) & 1, ctl);
-            if (!ok) break;
-            tc_fence_after();
-            issue_pv(t, vs, half, buf, i > 0);
-            if (more) issue_qk(t, ks, half, buf);
-            commit_if(lead, &bar->s_full[t][buf]);
-          }
+          ok = warp_wait(&bar->p_full[t][buf], (p_phase >> buf) & 1, ctl);
           if (!ok) break;
+          tc_fence_after();
+          issue_pv(vs, half, buf, i > 0);
+          if (more) issue_qk(ks, half, buf);
+          commit_if(lead, &bar->s_full[t][buf]);
           p_phase ^= 1u << buf;
           if (v_last) {
             commit_if(lead, &bar->v_empty[vs]);
