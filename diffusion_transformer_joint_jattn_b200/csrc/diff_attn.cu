@@ -60,7 +60,7 @@ constexpr float kRescaleThreshold = 15.0f;   // log2 units; P <= 2^15 in 16 bits
 // Every kPolyEvery-th pair of exponentials is done on the FMA pipe: at 16896
 // tokens x 6 heads all on the exponential unit took 1310 us, every 8th pair
 // 1270, every 4th 1290, every 3rd 1286 (the chip is at its power limit there).
-constexpr int kPolyEvery = 8;
+constexpr int kPolyEvery = 6;
 
 __host__ __device__ constexpr uint32_t col_s(int t, int buf) { return static_cast<uint32_t>(t * 128 + buf * 64); }
 __host__ __device__ constexpr uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(t) * 128u; }
@@ -115,6 +115,17 @@ __device__ __forceinline__ void tmem_st32_issue(uint32_t taddr, const uint32_t (
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
                ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
                : "memory");
+}
+__device__ __forceinline__ void tmem_st16_issue(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+               ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+               "tcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(taddr));
 }
 // The MMA and commit instructions by the lane with `lead` set.
 __device__ __forceinline__ void mma_ss_if(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -226,6 +237,17 @@ struct alignas(4 * E) Vec4or2 {
   float e[E];
 };
 
+// Of 16 or 32.
+template <int N>
+__device__ __forceinline__ float row_max(const float (&v)[N]) {
+  float a[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+  for (int i = 4; i < N; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = max3(a[k], v[i + k], v[i + 4 < N ? i + 4 + k : i + k]);
+  return max3(max3(a[0], a[1], a[2]), a[3], a[3]);
+}
+
 // V's largest finite magnitude per (batch entry, K/V head) over its allowed
 // keys, then its fp16 copy, zeros at masked keys: 8 channels of a row per
 // thread and step, blockIdx.y = the head, kConvRows rows per block.
@@ -282,6 +304,24 @@ __device__ __forceinline__ float lambda_of(const DiffParams& p, int head, int dm
     s2 += z.x * w.x + z.y * w.y + z.z * w.z + z.w * w.w;
   }
   return expf(s1) - expf(s2) + p.lambda_init;
+}
+
+// The same by a whole warp.
+__device__ __forceinline__ float lambda_by_warp(const DiffParams& p, int head, int dm) {
+  const int lane = threadIdx.x & 31;
+  const size_t plane = static_cast<size_t>(p.H) * dm;
+  float a1 = 0.f, a2 = 0.f;
+  for (int i = lane; i < dm; i += 32) {
+    const float* l = p.lam + static_cast<size_t>(head) * dm + i;
+    a1 = fmaf(l[0], l[plane], a1);
+    a2 = fmaf(l[2 * plane], l[3 * plane], a2);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a1 += __shfl_xor_sync(0xffffffffu, a1, o);
+    a2 += __shfl_xor_sync(0xffffffffu, a2, o);
+  }
+  return expf(a1) - expf(a2) + p.lambda_init;
 }
 
 // a / b of non-negative numbers, almost always small ones (64-bit divisions
@@ -417,11 +457,13 @@ enum : int {
 
 // QUAD: a range of at most 32 rows (a few queries, one each in the single-token
 // form).  They stand four times in the Q tile, once in each quarter of 32 TMEM
-// lanes, so that the work on them can be spread over the four schedulers: map
-// 0's softmax is warp 0's, map 1's warp 5's (left in the same quarter, both
-// would be one scheduler's), and with kBf16Split the low parts of P are the
-// business of warps 2 and 7, in their own rows: one P.V product instead of
-// two, the two results added at the end.  The other softmax warps rest.
+// lanes, so that the softmax of a half's 64 keys is spread over the four warps
+// of its map: each takes its columns of S, puts its P there and zeros in the
+// other columns of its rows, and has running maxima, sums and accumulator rows
+// of its own, which meet at the segment's end.  With kBf16Split two warps take
+// 32 columns each, and two more the same columns for P's low parts (one P.V
+// product instead of two); with kF16 each takes 16.  One warp per map and part
+// took 1340 of the 1550 clocks of a half, and bounded the walk at 5.4 TB/s.
 template <int D, int KIND, bool QUAD>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -460,11 +502,11 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     for (int t = 0; t < 2; ++t) {
       for (int i = 0; i < 2; ++i) {
         mbar_init(&bar->s_full[t][i], 1);
-        mbar_init(&bar->p_full[t][i], !QUAD ? BM / 32 : (KIND == kBf16Split ? 2 : 1));
+        mbar_init(&bar->p_full[t][i], BM / 32);
       }
-      mbar_init(&bar->exchange[t], !QUAD ? 2 * BM : (t == 0 ? 2 : 1));
+      mbar_init(&bar->exchange[t], QUAD ? 8 : 2 * BM);
     }
-    mbar_init(&bar->exchange[2], 1);
+    mbar_init(&bar->exchange[2], 8);
     for (int i = 0; i < 8; ++i) mbar_init(&bar->turn[0][i], 1);
     bar->abort = 0;
     fence_mbarrier_init();
@@ -506,19 +548,14 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       if (lane == 0) {
         int nq = 0, nk = 0;                             // Q tiles, key tiles (K and V) loaded so far
         bool v_behind = false;                          // the last key tile's V was not issued
-        bool lent = false;                              // QUAD: the Q tile serves the last segment's epilogue
-        uint32_t lent_phase = 0;
         Segment s;
         bool ok = true;
         for (Walk walk(p, share); ok && walk.next(p, share, s);) {
           if (s.n_kv == 0) continue;
           // the Q buffer is free once the previous segment's Q.K^T are done
           if (nq > 0 && !mbar_wait(&bar->q_empty, (nq - 1) & 1, ctl)) break;
-          if (QUAD && lent) {
-            if (!mbar_wait(&bar->exchange[2], lent_phase, ctl)) break;
-            lent_phase ^= 1u;
-          }
-          lent = s.whole;
+          // and, QUAD, once it has served that segment's epilogue
+          if (QUAD && nq > 0 && !mbar_wait(&bar->exchange[2], (nq - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(&bar->q_full, C::TB);
           for (int x = 0; x < C::NBOX; ++x) {
             if constexpr (QUAD) {
@@ -703,18 +740,26 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(regs_softmax<D>()));
     const int t = warp >> 2;                            // map of this warpgroup
-    // QUAD: the warp of this map that computes, and the one that has P's low parts
-    const bool hi_role = (warp & 3) == t, lo_role = KIND == kBf16Split && (warp & 3) == t + 2;
-    const bool works = !QUAD || hi_role || lo_role;
+    // QUAD: the key columns of a half that are this warp's, and whether it has P's low parts
+    constexpr int NC = !QUAD ? 64 : (KIND == kBf16Split ? 32 : 16);
+    const int group = !QUAD ? 0 : (KIND == kBf16Split ? warp & 1 : warp & 3);
+    const bool lo_role = KIND == kBf16Split && QUAD && ((warp >> 1) & 1) != t;
     const int row = QUAD ? lane : (warp & 3) * 32 + lane;   // of the tile; TMEM lane (warp & 3) * 32 + lane
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t to = lane_base + col_o(t);
     const float c_j = p.scale_log2;
+    constexpr int E = D / 32;                           // QUAD's epilogue: channels per lane
     const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
     uint32_t idx = 0, ex_phase = 0, turns = 0;
+    uint32_t segments = 0, pass_phase = 0;              // QUAD: with keys, so far; parity of exchange[1]
+    float norm_mine[E];                                 // QUAD: of channels lane * E on
+    if constexpr (QUAD) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) norm_mine[e] = p.norm_w != nullptr ? __ldg(p.norm_w + lane * E + e) : 1.f;
+    }
     Segment s;
     bool ok = true;
-    for (Walk walk(p, share); works && ok && walk.next(p, share, s);) {
+    for (Walk walk(p, share); ok && walk.next(p, share, s);) {
       const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(s.b) * p.S_kv : nullptr;
       const int r = s.rt * BM + row;                    // row of the range
       const bool live = r < p.R;
@@ -722,13 +767,19 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       const int head = s.gi * p.hpg + (live ? r / p.S_q : 0), s_q = live ? r % p.S_q : 0;
       const int n = s.n_half, key0 = s.t0 * BN;
       // needed at the end; read while the first tiles are on their way
-      const float lam = s.whole && live ? lambda_of(p, head, DM) : 0.f;
+      float lam = 0.f;
+      if constexpr (QUAD) {
+        if (s.whole && warp < p.R) lam = lambda_by_warp(p, s.gi * p.hpg + warp / p.S_q, DM);
+      } else {
+        if (s.whole && live) lam = lambda_of(p, head, DM);
+      }
       float m_run = -INFINITY, l_run = 0.f;
-      uint8_t mb[2] = {1, 1};
+      constexpr int MW = QUAD ? 1 : 2;
+      uint8_t mb[MW];
       auto load_mask = [&](int i) {
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int key = key0 + i * 64 + 32 * w + lane;
+        for (int w = 0; w < MW; ++w) {
+          const int key = key0 + i * 64 + group * NC + 32 * w + lane;
           mb[w] = key < p.S_kv ? __ldg(mask + key) : 0;
         }
       };
@@ -736,10 +787,12 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const uint32_t at = idx + i, buf = at & 1;
-        uint32_t keep[2] = {~0u, ~0u};
+        uint32_t keep[MW];
+#pragma unroll
+        for (int w = 0; w < MW; ++w) keep[w] = ~0u;
         if (mask != nullptr) {
 #pragma unroll
-          for (int w = 0; w < 2; ++w) keep[w] = __ballot_sync(0xffffffffu, mb[w] != 0);
+          for (int w = 0; w < MW; ++w) keep[w] = __ballot_sync(0xffffffffu, mb[w] != 0);
           if (i + 1 < n) load_mask(i + 1);
         }
         ok = warp_wait(&bar->s_full[t][buf], (at >> 1) & 1, ctl);
@@ -750,22 +803,24 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         tc_fence_after();
         const uint32_t ts = lane_base + col_s(t, buf);
-        float v[64];
+        float v[NC];
         {
-          uint32_t raw[64];
-          tmem_ld64(ts, raw);
+          uint32_t raw[NC];
+          if constexpr (NC == 64) tmem_ld64(ts, raw);
+          else if constexpr (NC == 32) tmem_ld32(ts + group * NC, raw);
+          else tmem_ld16(ts + group * NC, raw);
 #pragma unroll
-          for (int e = 0; e < 64; ++e) v[e] = __uint_as_float(raw[e]);
+          for (int e = 0; e < NC; ++e) v[e] = __uint_as_float(raw[e]);
         }
-        const int valid = s.len - key0 - i * 64;
-        if (valid < 64) {
+        const int valid = s.len - key0 - i * 64 - group * NC;
+        if (valid < NC) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
+          for (int e = 0; e < NC; ++e)
             if (e >= valid) v[e] = -INFINITY;
         }
-        if ((keep[0] & keep[1]) != ~0u) {
+        if ((keep[0] & keep[MW - 1]) != ~0u) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
+          for (int e = 0; e < NC; ++e)
             if (!((keep[e >> 5] >> (e & 31)) & 1u)) v[e] = -INFINITY;
         }
         const float mx = row_max(v) * c_j;
@@ -805,9 +860,9 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
         const float2 c2 = make_float2(c_j, c_j), nm2 = make_float2(neg_m, neg_m);
         float2 acc0 = make_float2(0.f, 0.f), acc1 = make_float2(0.f, 0.f);
-        uint32_t pk[32], lo[KIND == kBf16Split ? 32 : 1];
+        uint32_t pk[NC / 2], lo[KIND == kBf16Split ? NC / 2 : 1];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < NC / 2; ++c) {
           const float2 x = __ffma2_rn(make_float2(v[2 * c], v[2 * c + 1]), c2, nm2);
           const float2 e = c % kPolyEvery == kPolyEvery - 1 ? ex2_poly(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
           if (c & 1) acc1 = __fadd2_rn(acc1, e);
@@ -817,12 +872,24 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           if constexpr (KIND == kBf16Split)
             lo[c] = pack_x2<true>(e.x - __uint_as_float(pk[c] << 16), e.y - __uint_as_float(pk[c] & 0xFFFF0000u));
         }
-        if constexpr (KIND == kBf16Split && QUAD) {
+        if constexpr (!QUAD) {
+          tmem_st32_issue(ts, pk);
+          if constexpr (KIND == kBf16Split) tmem_st32_issue(ts + 32, lo);
+        } else if constexpr (KIND == kBf16Split) {
+          uint32_t zero[16];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) pk[c] = lo_role ? lo[c] : pk[c];
+          for (int c = 0; c < 16; ++c) {
+            pk[c] = lo_role ? lo[c] : pk[c];
+            zero[c] = 0u;
+          }
+          tmem_st16_issue(ts + group * 16, pk);
+          tmem_st16_issue(ts + (group ^ 1) * 16, zero);
+        } else {
+          uint32_t all[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) all[c] = c / 8 == group ? pk[c % 8] : 0u;
+          tmem_st32_issue(ts, all);
         }
-        tmem_st32_issue(ts, pk);
-        if constexpr (KIND == kBf16Split && !QUAD) tmem_st32_issue(ts + 32, lo);
         // passed earlier, among the last exponentials, it cost 3%
         if constexpr (!QUAD) arrive_if(lane == 0, &bar->turn[t ^ 1][warp & 3]);
         tmem_wait_st();
@@ -841,6 +908,126 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         idx += n + 2;
       }
       tc_fence_after();
+      if constexpr (QUAD) {
+        if (n == 0) {                                   // no key: zeros
+          for (int q = warp; q < p.R; q += 8) {
+            const int h = s.gi * p.hpg + q / p.S_q;
+            const size_t at = (static_cast<size_t>(s.b) * p.H + h) * p.S_q + q % p.S_q;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(
+                p.o + ((static_cast<size_t>(s.b) * p.S_q + q % p.S_q) * p.H + h) * D) + lane * (E / 2);
+#pragma unroll
+            for (int e = 0; e < E / 2; ++e) dst[e] = 0u;
+            if (p.lse != nullptr && lane < 2) p.lse[lane * rows + at] = -INFINITY;
+          }
+          continue;
+        }
+        // Every quarter of the TMEM lanes has its keys' part of every row.
+        // They meet in the Q tile's memory, [map][quarter][row][channel], eight
+        // rows at a time: warp w adds up row w of them.  The tile's last use
+        // has to be over for both maps; the producer loads it again after
+        // exchange[2].
+        ok = warp_wait(&bar->q_empty, segments & 1, ctl);
+        if (!ok) break;
+        float* meet = reinterpret_cast<float*>(sQ);
+        float2* sums = reinterpret_cast<float2*>(sL);   // [map][quarter][row]: maximum and sum
+        for (int r0 = 0; r0 < p.R; r0 += 8) {
+          const int mine = lane - r0;                   // this lane's row of the eight
+          if (r0 > 0) {
+            if (s.whole && r0 + warp < p.R) lam = lambda_by_warp(p, s.gi * p.hpg + (r0 + warp) / p.S_q, DM);
+            __syncwarp();
+            arrive_if(lane == 0, &bar->exchange[1]);
+            ok = warp_wait(&bar->exchange[1], pass_phase, ctl);
+            if (!ok) break;
+            pass_phase ^= 1u;
+          }
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t x[32];
+            __syncwarp();
+            tmem_ld32(to + c, x);
+            // channel quads at [quad ^ row]: eight rows of one quad share no bank
+            if (mine >= 0 && mine < 8) {
+              uint4* at = reinterpret_cast<uint4*>(meet + (warp * 8 + mine) * D);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                at[(c / 4 + e) ^ mine] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+          }
+          if (mine >= 0 && mine < 8) sums[warp * 8 + mine] = make_float2(m_run, l_run);
+          __syncwarp();
+          arrive_if(lane == 0, &bar->exchange[0]);
+          ok = warp_wait(&bar->exchange[0], ex_phase, ctl);
+          if (!ok) break;
+          ex_phase ^= 1u;
+          const int q = r0 + warp;
+          if (q >= p.R) continue;
+          float out[2][E], lse2[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float2 ml[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ml[k] = sums[(u * 4 + k) * 8 + warp];
+            const float m = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+            float l = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[u][e] = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float w = ml[k].x == -INFINITY ? 0.f : ex2_approx(ml[k].x - m);
+              // with P in two parts, quarters 2 u and 2 u + 1 have the first ones and the sums
+              if (KIND != kBf16Split || k / 2 == u) l = fmaf(w, ml[k].y, l);
+              const float* at = meet + ((u * 4 + k) * 8 + warp) * D + (((lane * E) / 4) ^ warp) * 4 + lane * E % 4;
+              if (w == 0.f && ml[k].y == 0.f) continue; // no key of this quarter
+#pragma unroll
+              for (int e = 0; e < E; ++e) out[u][e] = fmaf(w, at[e], out[u][e]);
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            lse2[u] = l == 0.f ? -INFINITY : m + __log2f(l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) out[u][e] *= inv;
+          }
+          if (!s.whole) {
+            // this part's normalised output and log-sum-exp of each map
+            const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.from_start ? 1 : 0);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float* dst = p.part_o + ((slot * 2 + u) * BM + q) * D + lane * E;
+#pragma unroll
+              for (int e = 0; e < E; ++e) dst[e] = out[u][e];
+              if (lane == 0) p.part_l[(slot * 2 + u) * BM + q] = lse2[u];
+            }
+            continue;
+          }
+          const int h = s.gi * p.hpg + q / p.S_q;
+          float y[E], sq = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            y[e] = fmaf(-lam, out[1][e], out[0][e]);
+            sq = fmaf(y[e], y[e], sq);
+          }
+          if (p.norm_w != nullptr) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            const float f = rsqrtf(sq * (1.f / D) + p.eps) * (1.f - p.lambda_init);
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] *= f * norm_mine[e];
+          }
+          uint32_t* dst = reinterpret_cast<uint32_t*>(
+              p.o + ((static_cast<size_t>(s.b) * p.S_q + q % p.S_q) * p.H + h) * D) + lane * (E / 2);
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) dst[e] = pack_x2<true>(y[2 * e], y[2 * e + 1]);
+          if (p.lse != nullptr && lane < 2)
+            p.lse[lane * rows + (static_cast<size_t>(s.b) * p.H + h) * p.S_q + q % p.S_q] =
+                (lane == 0 ? lse2[0] : lse2[1]) * 0.69314718055994531f;
+        }
+        if (!ok) break;
+        ++segments;
+        tc_fence_before();                              // before the next segment's P.V overwrites O_t
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        arrive_if(lane == 0, &bar->exchange[2]);
+        continue;
+      }
       float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       if constexpr (KIND == kBf16WideV)                 // undo V's power of two
         inv *= pow2(v_exponent(__ldg(p.v_amax + static_cast<size_t>(s.b) * p.H_kv + kv_head(s.gi))));
@@ -849,8 +1036,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // this part's normalised output and log-sum-exp of its map
         const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (s.from_start ? 1 : 0);
         if (warp_live) {
-          // QUAD: the low parts' product in rows 64 on, added by the merge
-          float* dst = p.part_o + ((slot * 2 + t) * BM + row + (QUAD && lo_role ? 64 : 0)) * D;
+          float* dst = p.part_o + ((slot * 2 + t) * BM + row) * D;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -867,7 +1053,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                              : "memory");
             }
           }
-          if (live && !(QUAD && lo_role)) p.part_l[(slot * 2 + t) * BM + row] = lse2;
+          if (live) p.part_l[(slot * 2 + t) * BM + row] = lse2;
         }
         tc_fence_before();                              // before the next segment's P.V overwrites O_t
         continue;
@@ -876,86 +1062,6 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       float* lse_row = p.lse != nullptr && live
                            ? p.lse + static_cast<size_t>(t) * rows + (static_cast<size_t>(s.b) * p.H + head) * p.S_q + s_q
                            : nullptr;
-      if constexpr (QUAD) {
-        if (lse_row != nullptr && hi_role) *lse_row = lse2 * 0.69314718055994531f;
-        if (n == 0) {                                   // no key: zeros, and no Q tile to lend
-          if (t == 0 && hi_role && live)
-            for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>(o_row + c) = make_uint4(0u, 0u, 0u, 0u);
-          continue;
-        }
-        // The maps' rows lie in different lanes: they meet in the Q tile's
-        // memory, [map][channel][row], whose last use is over and which the
-        // producer does not load again before exchange[2].
-        float* meet = reinterpret_cast<float*>(sQ) + t * D * 32 + lane;
-        if (lo_role) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t x[32];
-            tmem_ld32(to + c, x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) meet[(c + e) * 32] = __uint_as_float(x[e]);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          tc_fence_before();
-          __syncwarp();
-          arrive_if(lane == 0, &bar->exchange[0]);
-          continue;
-        }
-        if constexpr (KIND == kBf16Split) {
-          ok = warp_wait(&bar->exchange[0], ex_phase, ctl);
-          if (!ok) break;
-        }
-        const float w = t == 0 ? inv : -lam * inv;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t x[32];
-          __syncwarp();
-          tmem_ld32(to + c, x);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float low = KIND == kBf16Split ? meet[(c + e) * 32] : 0.f;
-            meet[(c + e) * 32] = (__uint_as_float(x[e]) + low) * w;
-          }
-        }
-        tc_fence_before();
-        if (t == 1) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          arrive_if(lane == 0, &bar->exchange[1]);
-        } else {
-          ok = warp_wait(&bar->exchange[1], ex_phase, ctl);
-          if (!ok) break;
-          float sq = 0.f;
-#pragma unroll 8
-          for (int c = 0; c < D; ++c) {
-            const float x = meet[c * 32] + meet[(D + c) * 32];
-            sq = fmaf(x, x, sq);
-          }
-          const float f = p.norm_w != nullptr ? rsqrtf(sq * (1.f / D) + p.eps) * (1.f - p.lambda_init) : 1.f;
-          if (live) {
-#pragma unroll 2
-            for (int c = 0; c < D; c += 8) {
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                float a = (meet[(c + 2 * e) * 32] + meet[(D + c + 2 * e) * 32]) * f;
-                float b = (meet[(c + 2 * e + 1) * 32] + meet[(D + c + 2 * e + 1) * 32]) * f;
-                if (p.norm_w != nullptr) {
-                  a *= __ldg(p.norm_w + c + 2 * e);
-                  b *= __ldg(p.norm_w + c + 2 * e + 1);
-                }
-                y[e] = pack_x2<true>(a, b);
-              }
-              *reinterpret_cast<uint4*>(o_row + c) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          arrive_if(lane == 0, &bar->exchange[2]);
-        }
-        ex_phase ^= 1u;
-        continue;
-      }
       sL[t * BM + row] = inv;
       tc_fence_before();
       mbar_arrive(&bar->exchange[0]);
@@ -1091,7 +1197,7 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[t][e] = 0.f;
   for (int i0 = sub; i0 < parts; i0 += WPR * kMergeParts) {
-    Chunk x[kMergeParts][2], y[kMergeParts][2];
+    Chunk x[kMergeParts][2];
     float w[kMergeParts][2];
 #pragma unroll
     for (int k = 0; k < kMergeParts; ++k) {
@@ -1103,7 +1209,6 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
         // a part without keys, or no part: weight 0
         w[k][t] = i0 + k * WPR < parts && l != -INFINITY ? ex2_approx(l - mx[t]) : 0.f;
         x[k][t] = *reinterpret_cast<const Chunk*>(p.part_o + at * D + lane * E);
-        if (p.low_rows) y[k][t] = *reinterpret_cast<const Chunk*>(p.part_o + (at + 64) * D + lane * E);
       }
     }
 #pragma unroll
@@ -1113,8 +1218,7 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
         if (w[k][t] == 0.f) continue;                   // its output may be unwritten
         tot[t] += w[k][t];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          acc[t][e] = fmaf(w[k][t], x[k][t].e[e] + (p.low_rows ? y[k][t].e[e] : 0.f), acc[t][e]);
+        for (int e = 0; e < E; ++e) acc[t][e] = fmaf(w[k][t], x[k][t].e[e], acc[t][e]);
       }
   }
   if constexpr (WPR > 1) {
@@ -1134,19 +1238,7 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
         tot[t] += sums[warp + k][t][D];
       }
   }
-  float a1 = 0.f, a2 = 0.f;
-  const size_t plane = static_cast<size_t>(p.H) * (D / 2);
-  for (int i = lane; i < D / 2; i += 32) {
-    const float* l = p.lam + static_cast<size_t>(head) * (D / 2) + i;
-    a1 = fmaf(l[0], l[plane], a1);
-    a2 = fmaf(l[2 * plane], l[3 * plane], a2);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a1 += __shfl_xor_sync(0xffffffffu, a1, o);
-    a2 += __shfl_xor_sync(0xffffffffu, a2, o);
-  }
-  const float lam = expf(a1) - expf(a2) + p.lambda_init;
+  const float lam = lambda_by_warp(p, head, D / 2);
   float out[E];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -1207,11 +1299,8 @@ cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorM
 template <int D>
 cudaError_t launch_d(const DiffParams& p, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, cudaStream_t st) {
-  if (p.R <= kQuadRows) {
-    DiffParams q = p;
-    q.low_rows = in_bf16;
-    return in_bf16 ? launch_t<D, kBf16Split, true>(q, tq, tk, tv, st) : launch_t<D, kF16, true>(q, tq, tk, tv, st);
-  }
+  if (p.R <= kQuadRows)
+    return in_bf16 ? launch_t<D, kBf16Split, true>(p, tq, tk, tv, st) : launch_t<D, kF16, true>(p, tq, tk, tv, st);
   if (!in_bf16) return launch_t<D, kF16>(p, tq, tk, tv, st);
   return p.v16 != nullptr ? launch_t<D, kBf16WideV>(p, tq, tk, tv, st) : launch_t<D, kBf16Split>(p, tq, tk, tv, st);
 }

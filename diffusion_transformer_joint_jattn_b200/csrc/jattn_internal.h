@@ -207,7 +207,6 @@ struct DiffParams {
   long long items_whole;        // the items below this number are walked whole, the others shared by all CTAs
   int ctas;                     // of the walk
   int merge;                    // items are shared: parts to merge
-  int low_rows;                 // set by the launcher: the parts' rows 64 on hold the products of P's low parts
   float scale_log2;
   const float* lam;             // [4][H][d / 2]
   float lambda_init;
