@@ -1163,32 +1163,50 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   const bool first = off > 0 && runs.start(cta - 1) <= g - off;
   const int range = static_cast<int>(divide(item, p.n_rt)), b = range / p.n_groups, gi = range % p.n_groups;
   const int r = static_cast<int>(item - static_cast<long long>(range) * p.n_rt) * BM + row;
+  const bool work = first && r < p.R;
+  // the last CTA that has a part of the item, by its last tile
+  const int parts = work ? runs.owner(g - off + tiles_of(p, b) - 1) - cta + 2 : 0;
+  const int head = work ? gi * p.hpg + r / p.S_q : 0, s_q = work ? r % p.S_q : 0;
+  const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
+  const size_t rg = (static_cast<size_t>(b) * p.H + head) * p.S_q + s_q;
+  const float lam = lambda_by_warp(p, head, D / 2);
+  float norm[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) norm[e] = p.norm_w != nullptr ? __ldg(p.norm_w + lane * E + e) : 1.f;
   // Everything above is the inputs' alone; the parts from here on.  Every block
   // waits for the walk, also one without work: this grid's end has to mean the
   // walk's end for what the stream holds next.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!first || r >= p.R) return;                       // WPR 4: the whole block
-  // the last CTA that has a part of the item, by its last tile
-  const int parts = runs.owner(g - off + tiles_of(p, b) - 1) - cta + 2;
-  const int head = gi * p.hpg + r / p.S_q, s_q = r % p.S_q;
-  const size_t rows = static_cast<size_t>(p.B) * p.H * p.S_q;
-  const size_t rg = (static_cast<size_t>(b) * p.H + head) * p.S_q + s_q;
+  if (!work) return;                                    // WPR 4: the whole block
   // part 0 is the end of CTA cta - 1's share, part i the start of cta + i - 1's
   auto part_at = [&](int i, int t) {
     const size_t slot = i == 0 ? 2 * static_cast<size_t>(cta - 1) + 1 : 2 * static_cast<size_t>(cta + i - 1);
     return (slot * 2 + t) * BM + row;
   };
+  Chunk x[kMergeParts][2];
+  float l[kMergeParts][2];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kMergeParts; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const size_t at = part_at(min(i0 + k * WPR, parts - 1), t);
+        l[k][t] = p.part_l[at];
+        x[k][t] = *reinterpret_cast<const Chunk*>(p.part_o + at * D + lane * E);
+      }
+  };
+  load(sub);                                            // on its way under the maxima's
   float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     for (int i = lane; i < parts; i += 32) {
-      const float l = p.part_l[part_at(i, t)];
-      mx[t] = l > mx[t] || l != l ? l : mx[t];          // a NaN stays
+      const float m = p.part_l[part_at(i, t)];
+      mx[t] = m > mx[t] || m != m ? m : mx[t];          // a NaN stays
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const float l = __shfl_xor_sync(0xffffffffu, mx[t], o);
-      mx[t] = l > mx[t] || l != l ? l : mx[t];
+      const float m = __shfl_xor_sync(0xffffffffu, mx[t], o);
+      mx[t] = m > mx[t] || m != m ? m : mx[t];
     }
   }
   float acc[2][E], tot[2] = {0.f, 0.f};
@@ -1196,30 +1214,21 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[t][e] = 0.f;
-  for (int i0 = sub; i0 < parts; i0 += WPR * kMergeParts) {
-    Chunk x[kMergeParts][2];
-    float w[kMergeParts][2];
-#pragma unroll
-    for (int k = 0; k < kMergeParts; ++k) {
-      const int i = min(i0 + k * WPR, parts - 1);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const size_t at = part_at(i, t);
-        const float l = p.part_l[at];
-        // a part without keys, or no part: weight 0
-        w[k][t] = i0 + k * WPR < parts && l != -INFINITY ? ex2_approx(l - mx[t]) : 0.f;
-        x[k][t] = *reinterpret_cast<const Chunk*>(p.part_o + at * D + lane * E);
-      }
-    }
+  for (int i0 = sub;;) {
 #pragma unroll
     for (int k = 0; k < kMergeParts; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (w[k][t] == 0.f) continue;                   // its output may be unwritten
-        tot[t] += w[k][t];
+        // a part without keys, or no part: weight 0, and its output may be unwritten
+        if (i0 + k * WPR >= parts || l[k][t] == -INFINITY) continue;
+        const float w = ex2_approx(l[k][t] - mx[t]);
+        tot[t] += w;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[t][e] = fmaf(w[k][t], x[k][t].e[e], acc[t][e]);
+        for (int e = 0; e < E; ++e) acc[t][e] = fmaf(w, x[k][t].e[e], acc[t][e]);
       }
+    i0 += WPR * kMergeParts;
+    if (i0 >= parts) break;
+    load(i0);
   }
   if constexpr (WPR > 1) {
 #pragma unroll
@@ -1238,7 +1247,6 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
         tot[t] += sums[warp + k][t][D];
       }
   }
-  const float lam = lambda_by_warp(p, head, D / 2);
   float out[E];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -1258,7 +1266,7 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
     for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
     const float f = rsqrtf(sq * (1.f / D) + p.eps) * (1.f - p.lambda_init);
 #pragma unroll
-    for (int e = 0; e < E; ++e) out[e] *= f * __ldg(p.norm_w + lane * E + e);
+    for (int e = 0; e < E; ++e) out[e] *= f * norm[e];
   }
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + ((static_cast<size_t>(b) * p.S_q + s_q) * p.H + head) * D) + lane * (E / 2);
 #pragma unroll
