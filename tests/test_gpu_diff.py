@@ -188,6 +188,54 @@ def test_large_logits_and_scale(cuda_device):
     assert np.linalg.norm(f(o) - want) <= (2.0 ** -8 + 2.0 ** -5) * np.linalg.norm(want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("S_q", [1, 4, 5, 16])
+def test_few_rows_by_key_columns(cuda_device, dtype, d, S_q):
+    """2 S_q rows, whose keys are spread over warps by their place in a half of
+    64: masks that leave one warp keys, all but one, a last half of few keys,
+    and one key alone; masked rows of k and v hold NaN."""
+    S = 1000
+    q, k, v, lam, w = make(cuda_device, dtype, 12, 2, 1, S_q, S, d, seed=S_q)
+    place = np.arange(S) % 64
+    allowed = np.stack([place // 16 == i for i in range(4)] + [place // 16 != i for i in range(4)] +
+                       [place < 32, place >= 32, place == 47, np.arange(S) == 990])
+    m = torch.from_numpy(allowed).to(cuda_device)
+    kk, vv = (torch.where(m[:, None, :, None], t, torch.full_like(t, float("nan"))) for t in (k, v))
+    zero = lambda t: torch.where(m[:, None, :, None], t, 0)  # noqa: E731
+    o, lse = jattn.fwd_diff(q, kk, vv, lam, INIT, norm_w=w, eps=EPS, key_mask=m, want_lse=True)
+    check(o, lse, q, zero(k), zero(v), lam, w, allowed)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("S_q", [1, 4, 16])
+def test_few_rows_large_logits(cuda_device, dtype, S_q):
+    """As test_large_logits_and_scale: the maxima of a row's key columns move by
+    themselves, in one CTA and across several."""
+    for S in (600, 2300):
+        q, k, v, lam, _ = make(cuda_device, dtype, 2, 4, 2, S_q, S, 128, seed=5)
+        for t in (q, k):
+            t.mul_(2)
+        o, lse = jattn.fwd_diff(q, k, v, lam, INIT, want_lse=True, softmax_scale=1.0)
+        f = lambda t: t.double().cpu().numpy()  # noqa: E731
+        want, lref, _ = ref.diff_attention(f(q), f(k), f(v), f(lam), INIT, scale=1.0)
+        assert np.abs(f(lse) - lref).max() <= 2.0 ** -5
+        assert np.linalg.norm(f(o) - want) <= (2.0 ** -8 + 2.0 ** -5) * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_repeat(cuda_device, d):
+    """CTAs that go from range to range reuse the memory of the queries: the
+    same call gives the same bits every time."""
+    q, k, v, lam, w = make(cuda_device, "bf16", 96, 4, 2, 9, 300, d)
+    n = torch.arange(96, dtype=torch.int32, device=cuda_device) * 3 + 1
+    first, l0 = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, kv_len=n, want_lse=True)
+    check(first, l0, q, k, v, lam, w, np.arange(300)[None] < n.cpu().numpy()[:, None])
+    for _ in range(50):
+        o, lse = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w, kv_len=n, want_lse=True)
+        assert torch.equal(o, first) and torch.equal(lse, l0)
+
+
 def test_nan_and_infinite_logits_stay_in_their_rows(cuda_device):
     """A query of NaN, one whose logit with some key is +inf, in every column of a
     key half (some exponentials are computed another way): NaN in that row's
