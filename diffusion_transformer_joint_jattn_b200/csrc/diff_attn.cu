@@ -18,9 +18,11 @@
 //               each: both maps' accumulators lie in the same TMEM lanes, so
 //               only the row sums and the norm's partial sums of squares go
 //               through shared memory.
-//   warp 8      MMA issuer, warp 9 TMA producer, warp 10 zeroes the V rows of
-//               masked keys in shared memory (their P is 0, and 0 * NaN would
-//               not be); warp 11 finds the CTA's share of the work.
+//   warp 8      issues map 0's products, warp 11 map 1's, after it has found
+//               the CTA's share of the work (one warp for both maps: 8 single
+//               queries over 16384 keys took 111 us, so 104; prompts 1% more);
+//               warp 9 TMA producer, warp 10 zeroes the V rows of masked keys
+//               in shared memory (their P is 0, and 0 * NaN would not be).
 // Keys are walked in halves of 64: each map has two S buffers of 64 TMEM
 // columns, and Q.K^T of half i + 2 is issued behind P.V of half i, so S of
 // half i + 1 is there when the softmax of half i ends and the softmax warps
@@ -57,9 +59,10 @@ template <int D> __host__ __device__ constexpr uint32_t regs_softmax() { return 
 template <int D> __host__ __device__ constexpr uint32_t regs_other() { return (kThreads * 168u - 256u * regs_softmax<D>()) / 128u; }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 15.0f;   // log2 units; P <= 2^15 in 16 bits
-// Every kPolyEvery-th pair of exponentials is done on the FMA pipe: at 16896
-// tokens x 6 heads all on the exponential unit took 1310 us, every 8th pair
-// 1270, every 4th 1290, every 3rd 1286 (the chip is at its power limit there).
+// Every kPolyEvery-th pair of exponentials is done on the FMA pipe: at 48 heads
+// x 4608 and 6 x 16896 tokens every 8th pair took 886 and 1308 us, every 6th
+// 880 and 1298, every 5th 887 and 1318, every 4th 896 and 1304; all on the
+// exponential unit 3% more than every 8th.
 constexpr int kPolyEvery = 6;
 
 __host__ __device__ constexpr uint32_t col_s(int t, int buf) { return static_cast<uint32_t>(t * 128 + buf * 64); }
