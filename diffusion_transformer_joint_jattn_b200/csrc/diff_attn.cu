@@ -542,8 +542,11 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   auto kv_head = [&](int gi) { return static_cast<int>(static_cast<long long>(gi) * p.H_kv / p.n_groups); };
   // V rows of masked keys have to be zeroed: a mask, or a length inside the
   // cache (rows past the cache arrive as zeros from TMA; the converted V has
-  // its masked rows zeroed)
-  auto fixes = [&](const Segment& s) { return KIND != kBf16WideV && (p.key_mask != nullptr || s.len < p.S_kv); };
+  // its masked rows zeroed).  In such a call every V tile goes through the mask
+  // warp and the products wait for v_ready, in segments without a masked key
+  // too: v_full would let them release a stage that the mask warp has yet to
+  // pass, and a parity wait that misses a phase takes the next one for it.
+  const bool masks = KIND != kBf16WideV && (p.key_mask != nullptr || p.kv_len != nullptr);
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(regs_other<D>()));
@@ -636,7 +639,6 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       for (Walk walk(p, share); ok && walk.next(p, share, s);) {
         if (s.n_kv == 0) continue;
         const int n = s.n_half;
-        const bool fix = fixes(s);
         ok = warp_wait(&bar->q_full, nq & 1, ctl) && warp_wait(&bar->k_full[nk % C::KS], (nk / C::KS) & 1, ctl);
         if (!ok) break;
         tc_fence_after();
@@ -658,7 +660,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
           const int buf = (idx + i) & 1, half = i & 1;
           const bool more = i + 2 < n, v_last = half || i + 1 == n;
           if (!half) {
-            ok = warp_wait(fix ? &bar->v_ready[vs] : &bar->v_full[vs], v_par, ctl) &&
+            ok = warp_wait(masks ? &bar->v_ready[vs] : &bar->v_full[vs], v_par, ctl) &&
                  (!more || warp_wait(&bar->k_full[ks], k_par, ctl));
             if (!ok) break;
           }
@@ -693,17 +695,17 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
       }
     } else if (warp == kMaskWarp) {
       if constexpr (KIND != kBf16WideV) {
-        if (p.key_mask != nullptr || p.kv_len != nullptr) {
+        if (masks) {
           int nv = 0;
           Segment s;
           bool ok = true;
           for (Walk walk(p, share); ok && walk.next(p, share, s);) {
-            const bool fix = fixes(s);
+            const bool fix = p.key_mask != nullptr || s.len < p.S_kv;
             const uint8_t* mask = p.key_mask != nullptr ? p.key_mask + static_cast<size_t>(s.b) * p.S_kv : nullptr;
             for (int j = 0; j < s.n_kv; ++j, ++nv) {
               const int vs = nv % C::VS, key0 = (s.t0 + j) * BN;
               if (!fix) {
-                // keep v_ready's phase with the stage's
+                // no masked key in this segment
                 ok = warp_wait(&bar->v_full[vs], (nv / C::VS) & 1, ctl);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(&bar->v_ready[vs]);

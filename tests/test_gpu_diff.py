@@ -317,3 +317,27 @@ def test_other_stream_and_graph(cuda_device):
             g.replay()
         want, _ = jattn.fwd_diff(q, k, v, lam, INIT, norm_w=w)
         assert all(torch.equal(o, want) for o in outs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("S_q", [1, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_full_and_short_caches_in_turn(cuda_device, dtype, d, S_q):
+    """CTAs that go from caches without a masked key to short or masked ones and
+    back: the V tiles of both kinds share one ring, and the rows that take no
+    part hold NaN.  The same bits every time."""
+    B, S = 90, 1500
+    q, k, v, lam, w = make(cuda_device, dtype, B, 4, 2, S_q, S, d, seed=d)
+    lens = np.where(np.arange(B) % 3 == 1, S, np.arange(B) * 97 % (S - 1))
+    lens[20:30] = S
+    allowed = np.arange(S)[None] < lens[:, None]
+    n = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    keep = torch.from_numpy(allowed).to(cuda_device)[:, None, :, None]
+    bad = torch.full_like(v, float("nan"))
+    vv, kk = torch.where(keep, v, bad), torch.where(keep, k, bad)
+    zero = torch.zeros_like(v)
+    o, lse = jattn.fwd_diff(q, kk, vv, lam, INIT, norm_w=w, eps=EPS, kv_len=n, want_lse=True)
+    check(o, lse, q, torch.where(keep, k, zero), torch.where(keep, v, zero), lam, w, allowed)
+    for _ in range(20):
+        again, _ = jattn.fwd_diff(q, kk, vv, lam, INIT, norm_w=w, eps=EPS, kv_len=n)
+        assert torch.equal(again, o)
