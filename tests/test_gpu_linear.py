@@ -179,3 +179,22 @@ def test_other_stream_and_graph(cuda_device):
         x.neg_()
         graph.replay()
         assert torch.equal(y, jattn.linear(x, w, b))
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("M", [17, 200])
+def test_gelu_of_negative_values(cuda_device, out, M):
+    """x = value * 1 where x Phi(x) is small and has to keep its relative
+    accuracy.  The exponent x^2 / 2 is off by at most 2^-23 relative (two
+    roundings), which moves the exponential by x^2 / 2 times that; its own
+    2^-22, the polynomial's 2^-22.5, the reciprocal and the products: under
+    (x^2 + 8) 2^-23."""
+    vals = torch.tensor([-0.25, -1.0, -2.0, -2.5, -3.0, -3.5, -4.0, -4.5, -5.0, -5.5, -6.0, -7.0, -8.0, -10.0, -12.0, 3.0, 6.0])
+    x = vals.bfloat16().repeat(-(-M // len(vals)))[:M].view(-1, 1).to(cuda_device)
+    w = torch.ones(40, 1, dtype=torch.bfloat16, device=cuda_device)
+    v = x.double().cpu().numpy()
+    want = torch.from_numpy(ref.activation(v, "gelu"))
+    got = jattn.linear(x, w, act="gelu", out_dtype=DT[out]).double().cpu()
+    t = torch.finfo(DT[out])
+    tol = (t.eps / 2 + torch.from_numpy(v * v + 8) * 2.0 ** -23) * want.abs() + t.smallest_normal * t.eps / 2
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol)[:17, 0]
