@@ -690,7 +690,8 @@ def rotary_freqs(dim=None, theta: float = 10000.0, scaling: str = "none", factor
               the fastest keeps its frequency
       yarn    pairs that turn at least ``fast_turns`` times over the original
               length keep their frequency, those below ``slow_turns`` are
-              interpolated, a linear ramp between; scale 0.1 ln(factor) + 1.
+              interpolated, a linear ramp between; scale 0.1 ln(factor) + 1
+              (1 for a factor up to 1: nothing is stretched).
     """
     if scaling not in ("none", "linear", "ntk", "yarn"):
         raise ValueError(f"unknown scaling {scaling!r}")
@@ -716,7 +717,7 @@ def rotary_freqs(dim=None, theta: float = 10000.0, scaling: str = "none", factor
             low, high = max(0, math.floor(at[0])), min(n - 1, math.ceil(at[1]))
             slow = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
             w = w / factor * slow + w * (1 - slow)
-            scale = 0.1 * math.log(factor) + 1.0
+            scale = 0.1 * math.log(max(factor, 1.0)) + 1.0
         freqs.append(w)
     return torch.cat(freqs).to("cuda" if device is None else device), scale
 

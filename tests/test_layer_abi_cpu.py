@@ -170,3 +170,11 @@ def test_host_tensors_are_refused():
         jattn.joint_attention(qkv, None, None, pos, (16, 24, 24), proj_w=torch.zeros(8, 128, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         jattn.joint_attention(qkv, None, None, pos, (16, 24, 24), residual=torch.zeros(1, 4, 8, dtype=torch.bfloat16))
+
+
+def test_yarn_scale_of_shorter_contexts():
+    """The factor of cosine and sine makes up for a stretched context: there is
+    none for a factor of 1 or less."""
+    for factor in (0.25, 0.5, 1.0):
+        assert jattn.rotary_freqs(64, scaling="yarn", factor=factor, device="cpu")[1] == 1.0
+    assert jattn.rotary_freqs(64, scaling="yarn", factor=2.0, device="cpu")[1] == 0.1 * math.log(2.0) + 1.0
