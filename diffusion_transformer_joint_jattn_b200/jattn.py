@@ -906,8 +906,9 @@ def fwd_diff(q, k, v, lam, lambda_init: float, norm_w=None, eps: float = 1e-5, k
              lse=None, want_lse: bool = False, softmax_scale: float = 0.0, workspace=None, stream=None):
     """Differential attention (jattn_fwd_diff): O = softmax(Q1 K1^T) V -
     lambda_h softmax(Q2 K2^T) V for q [B, H, S_q, d], k and v [B, H_kv, S_kv, d]
-    (fp16 or bf16, strided, channels contiguous; d 64 or 128, each map takes
-    half of q's and k's channels).
+    (fp16 or bf16, strided by multiples of 8 elements and at least d, so not
+    expanded, channels contiguous; d 64 or 128, each map takes half of q's and
+    k's channels).
 
     lam: fp32 [4, H, d / 2], lambda_h = exp(lam0 . lam1) - exp(lam2 . lam3) +
     lambda_init.  norm_w (fp32 [d]): RMSNorm of every head's output, times

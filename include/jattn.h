@@ -448,7 +448,9 @@ jattn_status jattn_linear(const jattn_linear_shape* shape, const void* x, const 
                           const void* residual, void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Differential attention's shape.  Strides in elements over (batch entry,
- * head, token), multiples of 8; channels contiguous.  d in {64, 128};
+ * head, token), multiples of 8 and at least d where the dimension has more than
+ * one element (an expanded k or v, stride 0, is JATTN_ERR_INVALID_ARG); channels
+ * contiguous.  d in {64, 128};
  * H_kv >= 1 divides H; B, S_q, S_kv >= 0 (S_kv 0: every row is empty),
  * S_q, S_kv <= 2^24, B * H <= 65535, (H / H_kv) * S_q <= 2^30. */
 typedef struct {
