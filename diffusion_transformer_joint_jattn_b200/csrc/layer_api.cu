@@ -189,6 +189,9 @@ jattn_status jattn_rotary(const jattn_rotary_tensor* tensors, int32_t n_tensors,
     if (p.x[t] == nullptr || p.y[t] == nullptr) return JATTN_ERR_INVALID_ARG;
     if (!aligned(p.x[t], elem_bytes(dtype)) || !aligned(p.y[t], elem_bytes(dtype))) return JATTN_ERR_ALIGNMENT;
   }
+  // a head of one tensor is written while another block reads the other tensor's
+  if (n_tensors == 2 && p.H[0] > 0 && p.H[1] > 0 && (p.y[0] == p.y[1] || p.y[0] == p.x[1] || p.y[1] == p.x[0]))
+    return JATTN_ERR_INVALID_ARG;
   p.B = B;
   p.S = S;
   p.d = d;
@@ -291,6 +294,8 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   const size_t need = L.total;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return JATTN_ERR_INVALID_ARG;
   if (need > 0 && !aligned(workspace, 256)) return JATTN_ERR_ALIGNMENT;
+  // a tile's rows are written while others read q, k and v
+  if (o == q || (s->S_kv > 0 && (o == k || o == v))) return JATTN_ERR_INVALID_ARG;
   jattn::DiffParams p{};
   p.B = s->B;
   p.H = s->H;

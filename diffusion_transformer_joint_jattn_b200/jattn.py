@@ -736,7 +736,8 @@ def rotary(q, k, pos, freqs, split: Optional[Sequence[int]] = None, layout: str 
     rotated channels.  ``inverse`` applies the transposed map: the gradient
     of the inputs from that of the outputs.
     out: (q_out, k_out) of the inputs' shapes and any strides, which may be
-    the inputs themselves; new contiguous tensors when None.
+    the inputs themselves, each its own, and otherwise overlap neither input;
+    new contiguous tensors when None.
     Returns (q_out, k_out)."""
     dev = q.get_device()
     if dev < 0:

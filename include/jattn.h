@@ -366,8 +366,8 @@ typedef enum { JATTN_ROTARY_INTERLEAVED = 0, JATTN_ROTARY_HALF = 1 } jattn_rotar
 
 /* One tensor to rotate: x [B, S, H, d] -> y, strides in elements over (batch
  * entry, token, head); the d channels of a head are contiguous.  y may be x
- * with the same strides; otherwise the two must not overlap, and y must not
- * overlap itself.  Pointers aligned to their element; 16-byte aligned ones
+ * with the same strides; otherwise no y overlaps an x (the other tensor's
+ * included), another y or itself.  Pointers aligned to their element; 16-byte aligned ones
  * with strides of whole 16 bytes are moved 16 bytes at a time. */
 typedef struct {
   const void* x;
@@ -479,6 +479,7 @@ typedef struct {
  *   o        : bf16 [B, S_q, H, d] contiguous.  A row without a key is zeros.
  *   lse      : fp32 [2][B][H][S_q], the natural-log sum-exp of both maps
  *              (-inf for a row without a key), or NULL.
+ *   o and lse overlap no input and not each other.
  *   softmax_scale <= 0 selects 1 / sqrt(d / 2).
  *   workspace: device scratch of at least jattn_fwd_diff_workspace()
  *              bytes, 256-byte aligned (NULL where that is 0).  Calls that

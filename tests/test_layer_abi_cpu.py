@@ -178,3 +178,18 @@ def test_yarn_scale_of_shorter_contexts():
     for factor in (0.25, 0.5, 1.0):
         assert jattn.rotary_freqs(64, scaling="yarn", factor=factor, device="cpu")[1] == 1.0
     assert jattn.rotary_freqs(64, scaling="yarn", factor=2.0, device="cpu")[1] == 0.1 * math.log(2.0) + 1.0
+
+
+def test_outputs_over_inputs_are_refused():
+    """Rotary: one tensor's output over the other tensor; differential
+    attention: the output over q, k or v (valid calls otherwise)."""
+    def two(code, x0, y0, x1, y1, H1=2):
+        t = b"".join(jattn._ROTARY_TENSOR.pack(x, y, H, 384, 128, 64, 384, 128, 64) for x, y, H in ((x0, y0, 2), (x1, y1, H1)))
+        got = jattn.load().jattn_rotary(t, 2, jattn.BF16, 1, 3, 64, 1, 64, A, 0, None, A, 0, 1.0, 0, None)
+        assert got == code, got
+    two(INV, A, 2 * A, 3 * A, 2 * A)
+    two(INV, A, 2 * A, 3 * A, A)
+    two(INV, A, 3 * A, 3 * A, 2 * A)
+    two(INV, A, 3 * A, 3 * A, A)
+    for kw in (dict(o=A, q=A, k=2 * A, v=3 * A), dict(o=A, q=2 * A, k=A, v=3 * A), dict(o=A, q=2 * A, k=3 * A, v=A)):
+        diff(INV, **kw)
