@@ -187,7 +187,7 @@ struct LinearParams {
   int tiles_a, tiles_b, splits;
   int vec_y, vec_r;             // bytes of the widest aligned access of y's and residual's rows, 0 = elements
 };
-LinearPlan plan_linear(int M, int N, int K, bool out_f32);
+LinearPlan plan_linear(int M, int N, int K, int out_dtype);
 // tx, tw: 2-D maps with 64-element boxes of plan.pair ? 128 : (swap ? bn : 128) rows of x and
 // plan.pair ? bn / 2 : (swap ? 128 : bn) rows of w.
 cudaError_t launch_linear(LinearParams p, const LinearPlan& plan, const CUtensorMap& tx, const CUtensorMap& tw,

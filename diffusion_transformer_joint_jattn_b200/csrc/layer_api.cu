@@ -258,7 +258,7 @@ jattn_status jattn_linear(const jattn_linear_shape* s, const void* x, const void
     if (c.x) x = dst[0];
     if (c.w) w = dst[1];
   }
-  const jattn::LinearPlan plan = jattn::plan_linear(s->M, s->N, s->K, s->out_dtype == JATTN_FP32);
+  const jattn::LinearPlan plan = jattn::plan_linear(s->M, s->N, s->K, s->out_dtype);
   CUtensorMap tx, tw;
   const int bx = plan.pair ? 128 : (plan.swap ? plan.bn : 128), bw = plan.pair ? plan.bn / 2 : (plan.swap ? 128 : plan.bn);
   if (!matrix_map(&tx, x, s->M, s->K, c.x ? padded(s->K) : s->ldx, bx) ||

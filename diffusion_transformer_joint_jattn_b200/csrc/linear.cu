@@ -18,9 +18,11 @@
 //
 // The tensor cores' own fp32 sums lose a little at every addition (about half
 // a unit per 16 products, and always towards zero: 2e-6 of the result at K =
-// 3000), which a 16-bit output never shows.  For fp32 outputs the accumulator
-// is emptied every kFlushSteps K steps into fp32 registers that add with
-// rounding (FLUSH; two accumulators, so the products go on meanwhile).
+// 3000, 6e-3 at K = 2^20 where all products have one sign).  For fp32 outputs,
+// and for 16-bit ones of sums so long that it would show beside their rounding
+// (gathers), the accumulator is emptied every kFlushSteps K steps into fp32
+// registers that add with rounding (FLUSH; two accumulators, so the products go
+// on meanwhile).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -949,11 +951,19 @@ cudaError_t launch_pair(LinearParams p, const CUtensorMap& tx, const CUtensorMap
 
 }  // namespace
 
+// Whether the accumulator is emptied on the way.  K products of one sign lose
+// 5.4e-9 K of their sum (measured: 2304 x 2304, K = 2^16, 3.5e-4): a fifth of half
+// a step of fp16 at K = 2^14, of bf16 at 2^17.  Ungathered, fp16 results were off
+// by 1.7 times half a step at K = 2^16 and 13 times at 2^20.
+static bool gathers(int K, int out_dtype) {
+  return K > (out_dtype == JATTN_FP32 ? kFlushSteps * BK : (out_dtype == JATTN_FP16 ? 1 << 14 : 1 << 17));
+}
+
 // The kernel, tile and split of one problem: pure host arithmetic.
-LinearPlan plan_linear(int M, int N, int K, bool out_f32) {
+LinearPlan plan_linear(int M, int N, int K, int out_dtype) {
   LinearPlan pl{};
   const long long ksteps = (static_cast<long long>(K) + BK - 1) / BK;
-  pl.flush = out_f32 && ksteps > kFlushSteps;
+  pl.flush = gathers(K, out_dtype);
   const int pn = pl.flush ? 128 : 256;
   const long long pair_tiles = static_cast<long long>((M + 255) / 256) * ((N + pn - 1) / pn);
   // 256 x 256 tiles once they nearly fill the 74 pairs (1536 x 3000 x 1360, 72

@@ -198,3 +198,25 @@ def test_gelu_of_negative_values(cuda_device, out, M):
     t = torch.finfo(DT[out])
     tol = (t.eps / 2 + torch.from_numpy(v * v + 8) * 2.0 ** -23) * want.abs() + t.smallest_normal * t.eps / 2
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol)[:17, 0]
+
+
+@pytest.mark.parametrize("M,N,K,out", [
+    (4, 256, 1 << 18, "fp16"), (30, 130, 1 << 18, "fp16"), (300, 300, 1 << 18, "fp16"), (40, 70, 100001, "fp16"),
+    (2304, 2304, 1 << 17, "fp16"), (2304, 2304, 1 << 19, "bf16"), (300, 300, 1 << 20, "bf16"),
+])
+def test_long_sums_of_one_sign(cuda_device, M, N, K, out):
+    """Sums of so many products that the accumulator's losses would show in a
+    16-bit output.  Runs of 512 products (32 additions of at most 2^-23 of the
+    sum each), up to 2048 of them added with rounding in fp32 (2^-24 each, and
+    no more than a quarter of them one way)."""
+    g = torch.Generator(device=cuda_device).manual_seed(K)
+    x, w = (torch.empty(n, K, dtype=torch.bfloat16, device=cuda_device) for n in (M, N))
+    for t in (x, w):
+        for i in range(0, len(t), 256):
+            t[i:i + 256] = torch.rand(t[i:i + 256].shape, generator=g, device=cuda_device) / (K if t is w else 1)
+    y = jattn.linear(x, w, out_dtype=DT[out])
+    rows = torch.arange(0, M, max(1, M // 16), device=cuda_device)
+    want = sum(x[rows, i:i + 65536].double() @ w[:, i:i + 65536].double().t() for i in range(0, K, 65536))
+    tol = torch.finfo(DT[out]).eps / 2 + 2.0 ** -18 + K // 512 / 4 * 2.0 ** -24
+    assert ((y[rows].double() / want - 1).abs() <= tol).all()
+    assert jattn.device_status()[0] == jattn.OK
