@@ -59,6 +59,11 @@ template <int D> __host__ __device__ constexpr uint32_t regs_softmax() { return 
 template <int D> __host__ __device__ constexpr uint32_t regs_other() { return (kThreads * 168u - 256u * regs_softmax<D>()) / 128u; }
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 15.0f;   // log2 units; P <= 2^15 in 16 bits
+// Every kGatherKeys / 64 halves a row's accumulator is added to fp32 sums in the
+// workspace and starts again from zero: the tensor cores' own sums lose a part of
+// a unit at every addition, always towards zero, 6e-9 of the result per key (whole
+// walks over 2^18 and 2^20 keys were 1.6e-3 and 6.6e-3 too small).
+constexpr int kGather = kGatherKeys / 64;
 // Every kPolyEvery-th pair of exponentials is done on the FMA pipe: at 48 heads
 // x 4608 and 6 x 16896 tokens every 8th pair took 886 and 1308 us, every 6th
 // 880 and 1298, every 5th 887 and 1318, every 4th 896 and 1304; all on the
@@ -397,6 +402,40 @@ struct Runs {
   }
 };
 
+// A thread's row of the accumulator at `to` and its sums in the workspace, in
+// units of 2^(its maximum then) with `any`, else none yet.  OUT: the accumulator
+// is added to the sums and set to zero; otherwise the sums to the accumulator.
+template <int D, bool OUT>
+__device__ __forceinline__ void gather_row(const DiffParams& p, uint32_t to, float m_run, bool any) {
+  const size_t at = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  float* sums = p.sums + at * D;
+  const float m = any ? p.sums_m[at] : -INFINITY;
+  const float f = m == -INFINITY ? 0.f : ex2_approx(m - m_run);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t o[32];
+    __syncwarp();
+    tmem_ld32(to + c, o);
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      float4* dst = reinterpret_cast<float4*>(sums + c + e);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (any) x = *dst;
+      x.x = fmaf(x.x, f, __uint_as_float(o[e]));
+      x.y = fmaf(x.y, f, __uint_as_float(o[e + 1]));
+      x.z = fmaf(x.z, f, __uint_as_float(o[e + 2]));
+      x.w = fmaf(x.w, f, __uint_as_float(o[e + 3]));
+      if constexpr (OUT) *dst = x;
+      o[e] = OUT ? 0u : __float_as_uint(x.x);
+      o[e + 1] = OUT ? 0u : __float_as_uint(x.y);
+      o[e + 2] = OUT ? 0u : __float_as_uint(x.z);
+      o[e + 3] = OUT ? 0u : __float_as_uint(x.w);
+    }
+    tmem_st32(to + c, o);
+  }
+  if constexpr (OUT) p.sums_m[at] = m_run;
+}
+
 // One piece of work: key tiles [t0, t0 + n_kv) of an item.
 struct Segment {
   int b, gi, rt, len, t0, n_kv, n_half;
@@ -467,7 +506,11 @@ enum : int {
 // 32 columns each, and two more the same columns for P's low parts (one P.V
 // product instead of two); with kF16 each takes 16.  One warp per map and part
 // took 1340 of the 1550 clocks of a half, and bounded the walk at 5.4 TB/s.
-template <int D, int KIND, bool QUAD>
+//
+// LONG: S_kv > kGatherKeys, the walk that empties its accumulators on the way: a
+// kernel of its own, because the branch alone cost the shorter walks 4 to 8% and
+// these take 4% longer (148 row tiles over 2^18 keys: 3.62 -> 3.78 ms).
+template <int D, int KIND, bool QUAD, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const DiffParams p) {
@@ -853,6 +896,12 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             tmem_st32(to + c * 32, o);
           }
         }
+        if (LONG && i > 0 && i % kGather == 0) {
+          ok = warp_wait(&bar->s_full[t][buf ^ 1], ((at + 1) >> 1) & 1, ctl);
+          if (!ok) break;
+          tc_fence_after();
+          gather_row<D, true>(p, to, m_run, i > kGather);
+        }
         // The two warps of a scheduler (map 0's and map 1's of the same rows)
         // take the exponential unit in turns: left to themselves they fall into
         // step, want it at the same time and leave it idle at the same time.
@@ -913,6 +962,7 @@ diff_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         idx += n + 2;
       }
       tc_fence_after();
+      if (LONG && n > kGather && warp_live) gather_row<D, false>(p, to, m_run, true);
       if constexpr (QUAD) {
         if (n == 0) {                                   // no key: zeros
           for (int q = warp; q < p.R; q += 8) {
@@ -1278,12 +1328,12 @@ __global__ void __launch_bounds__(128) diff_merge_kernel(const DiffParams p, int
   for (int e = 0; e < E / 2; ++e) dst[e] = pack_x2<true>(out[2 * e], out[2 * e + 1]);
 }
 
-template <int D, int KIND, bool QUAD = false>
+template <int D, int KIND, bool QUAD, bool LONG>
 cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t st) {
   using C = Cfg<D>;
   static_assert(C::SMEM <= 232448, "shared memory budget");
-  auto kern = diff_attn_kernel<D, KIND, QUAD>;
+  auto kern = diff_attn_kernel<D, KIND, QUAD, LONG>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   if (KIND == kBf16WideV && p.S_kv > 0) {
@@ -1309,13 +1359,14 @@ cudaError_t launch_t(const DiffParams& p, const CUtensorMap& tq, const CUtensorM
   return cudaLaunchKernelEx(&cfg, diff_merge_kernel<D, WPR>, p, p.ctas);
 }
 
-template <int D>
+template <int D, bool LONG>
 cudaError_t launch_d(const DiffParams& p, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, cudaStream_t st) {
   if (p.R <= kQuadRows)
-    return in_bf16 ? launch_t<D, kBf16Split, true>(p, tq, tk, tv, st) : launch_t<D, kF16, true>(p, tq, tk, tv, st);
-  if (!in_bf16) return launch_t<D, kF16>(p, tq, tk, tv, st);
-  return p.v16 != nullptr ? launch_t<D, kBf16WideV>(p, tq, tk, tv, st) : launch_t<D, kBf16Split>(p, tq, tk, tv, st);
+    return in_bf16 ? launch_t<D, kBf16Split, true, LONG>(p, tq, tk, tv, st) : launch_t<D, kF16, true, LONG>(p, tq, tk, tv, st);
+  if (!in_bf16) return launch_t<D, kF16, false, LONG>(p, tq, tk, tv, st);
+  return p.v16 != nullptr ? launch_t<D, kBf16WideV, false, LONG>(p, tq, tk, tv, st)
+                          : launch_t<D, kBf16Split, false, LONG>(p, tq, tk, tv, st);
 }
 
 }  // namespace
@@ -1365,7 +1416,9 @@ bool diff_widens_v(long long items, int n_rt, int S_kv, int sms) {
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st) {
   static_assert(kQuadRows == 32, "one quarter of the TMEM lanes");
-  return d == 128 ? launch_d<128>(p, in_bf16, tq, tk, tv, st) : launch_d<64>(p, in_bf16, tq, tk, tv, st);
+  if (p.S_kv > kGatherKeys)
+    return d == 128 ? launch_d<128, true>(p, in_bf16, tq, tk, tv, st) : launch_d<64, true>(p, in_bf16, tq, tk, tv, st);
+  return d == 128 ? launch_d<128, false>(p, in_bf16, tq, tk, tv, st) : launch_d<64, false>(p, in_bf16, tq, tk, tv, st);
 }
 
 }  // namespace jattn

@@ -218,6 +218,8 @@ struct DiffParams {
   float* lse;                   // [2][B][H][S_q] or null
   float* part_o;                // [2 * ctas][2][128][d]: the parts of shared items
   float* part_l;                // [2 * ctas][2][128], log2 units
+  float* sums;                  // S_kv > kGatherKeys: [ctas][256][d], every softmax thread's sums of its row
+  float* sums_m;                // with sums: [ctas][256], the maxima they are relative to, log2 units
   const __nv_bfloat16* v;       // with v16: the bf16 values it is made from, and their strides in elements
   int64_t v_stride[3];          //   over (batch entry, head, token)
   __half* v16;                  // null, or [B][H_kv][S_kv][d]: fp16 copy of v, divided by a power of two per head
@@ -233,6 +235,8 @@ DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms);
 bool diff_widens_v(long long items, int n_rt, int S_kv, int sms);
 // Ranges of at most this many rows are walked by a kernel of their own.
 constexpr int kQuadRows = 32;
+// A row's accumulator is emptied after this many keys.
+constexpr int kGatherKeys = 32768;
 // The maps describe (d, rows, heads or ranges, batch) with boxes of 64 x 128 (q's: 64 x 32 where R <= kQuadRows).
 cudaError_t launch_diff_attn(const DiffParams& p, int d, bool in_bf16, const CUtensorMap& tq, const CUtensorMap& tk,
                              const CUtensorMap& tv, cudaStream_t st);

@@ -82,9 +82,10 @@ jattn_status diff_ranges(const jattn_diff_shape* s, DiffRanges* r) {
 }
 
 // Workspace segments, each 256-byte aligned: the splits' partial results, the
-// fp16 copy of V and its per-head magnitudes.
+// sums that long walks empty their accumulators into, the fp16 copy of V and its
+// per-head magnitudes.
 struct DiffLayout {
-  size_t part_o, part_l, v16, v_amax, total;
+  size_t part_o, part_l, sums, sums_m, v16, v_amax, total;
 };
 
 DiffLayout diff_layout(const jattn_diff_shape* s, const DiffRanges& r, bool in_bf16) {
@@ -94,6 +95,10 @@ DiffLayout diff_layout(const jattn_diff_shape* s, const DiffRanges& r, bool in_b
   if (r.walk.merge) {
     L.part_o = seg(static_cast<size_t>(r.walk.ctas) * 4 * 128 * s->d * 4);
     L.part_l = seg(static_cast<size_t>(r.walk.ctas) * 4 * 128 * 4);
+  }
+  if (s->S_kv > jattn::kGatherKeys) {
+    L.sums = seg(static_cast<size_t>(r.walk.ctas) * 256 * s->d * 4);
+    L.sums_m = seg(static_cast<size_t>(r.walk.ctas) * 256 * 4);
   }
   if (in_bf16 && r.widen) {
     L.v16 = seg(static_cast<size_t>(s->B) * s->H_kv * s->S_kv * s->d * 2);
@@ -324,6 +329,10 @@ jattn_status jattn_fwd_diff(const jattn_diff_shape* s, jattn_dtype in_dtype, con
   if (r.walk.merge) {
     p.part_o = reinterpret_cast<float*>(ws + L.part_o);
     p.part_l = reinterpret_cast<float*>(ws + L.part_l);
+  }
+  if (s->S_kv > jattn::kGatherKeys) {
+    p.sums = reinterpret_cast<float*>(ws + L.sums);
+    p.sums_m = reinterpret_cast<float*>(ws + L.sums_m);
   }
   const bool widen = in_bf16 && r.widen;
   if (widen) {

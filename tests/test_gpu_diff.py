@@ -341,3 +341,78 @@ def test_full_and_short_caches_in_turn(cuda_device, dtype, d, S_q):
     for _ in range(20):
         again, _ = jattn.fwd_diff(q, kk, vv, lam, INIT, norm_w=w, eps=EPS, kv_len=n)
         assert torch.equal(again, o)
+
+
+def of_rows(q, k, v, lam, b, h, rows, allowed=None):
+    """The definition in fp64 on the GPU, without the norm, of some rows of one
+    head: (o [rows, d], lse [2, rows])."""
+    n, d = h // (q.shape[1] // k.shape[1]), q.shape[3]
+    keep = slice(None) if allowed is None else allowed[b]
+    kk, vv = k[b, n][keep], v[b, n][keep].double()
+    f = [1.0, -(torch.exp(lam[0, h].double() @ lam[1, h].double()) - torch.exp(lam[2, h].double() @ lam[3, h].double())
+                + INIT)]
+    o, lse = 0.0, []
+    for m in range(2):
+        ch = slice(m * d // 2, (m + 1) * d // 2)
+        t = q[b, h, rows][:, ch].double() @ kk[:, ch].double().t() / (d // 2) ** 0.5
+        lse.append(torch.logsumexp(t, -1))
+        o = o + f[m] * (torch.softmax(t, -1) @ vv)
+    return o, torch.stack(lse)
+
+
+# Forms of the walk over 2^18 to 2^20 keys: (dtype, H, H_kv, S_q, S_kv).  One range of 148 row tiles, walked whole
+# (bf16: V copied to fp16); 50 ranges of three row tiles, some whole and the others shared (bf16: P in two parts); one
+# query per head, each CTA with more than 2^15 keys of a cache.
+LONG = [("fp16", 1, 1, 148 * 128, 1 << 20), ("bf16", 1, 1, 148 * 128, 1 << 20), ("bf16", 50, 1, 300, 1 << 18),
+        ("fp16", 50, 1, 300, 1 << 18), ("bf16", 16, 8, 1, 1 << 20), ("fp16", 16, 8, 1, 1 << 20)]
+
+
+def make_long(dev, dtype, H, H_kv, S_q, S_kv):
+    g = torch.Generator(device=dev).manual_seed(S_kv + H)
+    mk = lambda *s: torch.randn(*s, generator=g, device=dev, dtype=DT[dtype])  # noqa: E731
+    q = mk(1, S_q, H, 128).transpose(1, 2)                     # shared heads' rows not equally spaced: a range per head
+    lam = 0.2 * torch.randn(4, H, 64, generator=g, device=dev)
+    return q, mk(1, H_kv, S_kv, 128), mk(1, H_kv, S_kv, 128), lam
+
+
+@pytest.mark.parametrize("dtype,H,H_kv,S_q,S_kv", LONG)
+def test_long_walks_keep_their_sums(cuda_device, dtype, H, H_kv, S_q, S_kv):
+    """V the same at every key: every row's output is (1 - lambda) V, up to its
+    rounding and what the accumulator loses in runs of 2^15 keys -- for each 16
+    keys at most two units of 2^-23 of a sum that grows evenly, 2^-12."""
+    q, k, v, _ = make_long(cuda_device, dtype, H, H_kv, S_q, S_kv)
+    c = (1 + torch.arange(128, device=cuda_device) / 128).to(DT[dtype])
+    v.copy_(c)
+    o, lse = jattn.fwd_diff(q, k, v, torch.zeros(4, H, 64, device=cuda_device), INIT, want_lse=True)
+    err = (o.double() / ((1 - INIT) * c.double()) - 1).abs()
+    assert err.max() <= 2.0 ** -8 + 2.0 ** -11
+    assert torch.isfinite(lse).all() and jattn.device_status()[0] == jattn.OK
+
+
+@pytest.mark.parametrize("dtype,H,H_kv,S_q,S_kv", LONG)
+@pytest.mark.parametrize("how", ["growing", "masked"])
+def test_long_walks_against_the_definition(cuda_device, dtype, H, H_kv, S_q, S_kv, how):
+    """Maxima that move from run to run (keys that grow along the cache), and a
+    cache whose first runs, and most of the others, are masked.  The output's
+    rounding is spread evenly over a step, 2^-7 of a value with mantissa 1: at
+    most 2^-7 / sqrt(12) = 2.26e-3 in the L2 norm (outputs near 0.0713, mantissa
+    1.14, have 1.98e-3 of it); P's in fp16 adds 2e-4: 2.5e-3 together."""
+    q, k, v, lam = make_long(cuda_device, dtype, H, H_kv, S_q, S_kv)
+    v += 0.5
+    kw, allowed = {}, None
+    if how == "growing":
+        k *= torch.linspace(0.2, 2.0, S_kv, device=cuda_device).to(k.dtype)[:, None]    # linspace in fp16 is NaN
+    else:
+        m = torch.rand(1, S_kv, generator=torch.Generator(device=cuda_device).manual_seed(1), device=cuda_device) < 0.1
+        m[:, :S_kv // 3] = False
+        n = S_kv - 1000
+        kw = dict(key_mask=m, kv_len=torch.tensor([n], dtype=torch.int32, device=cuda_device))
+        allowed = m & (torch.arange(S_kv, device=cuda_device) < n)
+        v.masked_fill_(~allowed[:, None, :, None], float("nan"))
+    o, lse = jattn.fwd_diff(q, k, v, lam, INIT, want_lse=True, **kw)
+    for h in {0, H // 2, H - 1}:
+        rows = torch.tensor(sorted({0, S_q // 3, S_q - 1}), device=cuda_device)
+        want, lref = of_rows(q, k, v, lam, 0, h, rows, allowed)
+        assert (o[0, rows, h].double() - want).norm() <= 2.5e-3 * want.norm()
+        assert (lse[:, 0, h][:, rows].double() - lref).abs().max() <= 2.0 ** -13
+    assert jattn.device_status()[0] == jattn.OK

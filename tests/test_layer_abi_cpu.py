@@ -193,3 +193,14 @@ def test_outputs_over_inputs_are_refused():
     two(INV, A, 3 * A, 3 * A, A)
     for kw in (dict(o=A, q=A, k=2 * A, v=3 * A), dict(o=A, q=2 * A, k=A, v=3 * A), dict(o=A, q=2 * A, k=3 * A, v=A)):
         diff(INV, **kw)
+
+
+def test_diff_workspace_of_long_caches():
+    """Past 2^15 keys every CTA has fp32 sums of its 256 rows in the workspace."""
+    def size(S_kv, d):
+        return jattn.load().jattn_fwd_diff_workspace(
+            jattn._DIFF_SHAPE.pack(1, 1, 1, 128 * 160, S_kv, d, 128 * 160 * d, 128 * 160 * d, d,
+                                   *(2 * (S_kv * d, S_kv * d, d))), jattn.FP16)
+    for d in (64, 128):
+        sums = 148 * 256 * (d + 1) * 4
+        assert sums <= size(32769, d) - size(32768, d) <= sums + 512
