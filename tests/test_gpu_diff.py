@@ -416,3 +416,70 @@ def test_long_walks_against_the_definition(cuda_device, dtype, H, H_kv, S_q, S_k
         assert (o[0, rows, h].double() - want).norm() <= 2.5e-3 * want.norm()
         assert (lse[:, 0, h][:, rows].double() - lref).abs().max() <= 2.0 ** -13
     assert jattn.device_status()[0] == jattn.OK
+
+
+def near(o, want):
+    """As near to `want` in the L2 norm as its own rounding to bf16, plus 2^-12:
+    P in fp16 is off by 2^-11 / sqrt(3) = 2.8e-4 at most (evenly spread over a
+    step), which adds to the rounding's 1.5e-3 or more as squares do, 3e-5; P as
+    the sum of two bf16 by 2^-18, logits by 2^-16.  P in bf16 alone would add
+    0.7e-3 (1.7e-3 as squares), a key of 64 left out 0.1."""
+    own = (want.to(torch.bfloat16).double() - want).norm() / want.norm()
+    return ((o.double() - want).norm() / want.norm() <= own + 2.0 ** -12).item()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,H_kv,S_q,S_kv", [(1, 2, 2, 1, 5000), (1, 4, 1, 8, 3001), (2, 2, 2, 40, 5000),
+                                               (1, 2, 1, 300, 4100), (1, 40, 40, 512, 2400), (60, 4, 2, 9, 700)])
+def test_precision_of_the_probabilities(cuda_device, dtype, d, B, H, H_kv, S_q, S_kv):
+    """Long rows, V random, and V zero but for one 64-key half at a time (the
+    first ones, both of a tile in the middle, the last): every half's keys meet
+    their own V rows, with all the precision that P is held in."""
+    q, k, v, lam, _ = make(cuda_device, dtype, B, H, H_kv, S_q, S_kv, d, seed=S_kv)
+    rows = torch.arange(S_q, device=cuda_device)
+    last = (S_kv - 1) // 64
+    for half in (None, 0, 1, last // 2, last // 2 + 1, last):
+        vv = v
+        if half is not None:
+            vv = torch.zeros_like(v)
+            vv[:, :, 64 * half:64 * half + 64] = v[:, :, 64 * half:64 * half + 64]
+        o, _ = jattn.fwd_diff(q, k, vv, lam, INIT)
+        for b, h in {(0, 0), (B // 2, H // 2), (B - 1, H - 1)}:
+            assert near(o[b, :, h], of_rows(q, k, vv, lam, b, h, rows)[0]), (half, b, h)
+
+
+@pytest.mark.parametrize("dtype,G,H_kv", [("bf16", 2, 19), ("bf16", 2, 23), ("bf16", 1, 38), ("bf16", 1, 45), ("fp16", 2, 23),
+                                          ("fp16", 1, 45)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_whole_items_and_a_shared_tail(cuda_device, dtype, d, G, H_kv):
+    """Ranges of several row tiles, most walked whole and the last wave shared by
+    all CTAs; with two heads per K/V head (four row tiles) a bf16 V is copied to
+    fp16 by powers of two, else P is in two parts.  Lengths and a mask, NaN in
+    masked rows; the tail's rows against the definition."""
+    B, S_q, S_kv = 2, 250, 2300
+    n_rt, tiles = -(-G * S_q // 128), -(-S_kv // 128)
+    items, sms = B * H_kv * n_rt, torch.cuda.get_device_properties(0).multi_processor_count
+    rest = items % sms
+    assert items > sms and rest > 0 and (sms - rest) * tiles > 8 * sms             # a tail that is shared
+    q, k, v, lam, _ = make(cuda_device, dtype, B, G * H_kv, H_kv, S_q, S_kv, d, seed=H_kv)
+    need = jattn.load().jattn_fwd_diff_workspace(
+        jattn._DIFF_SHAPE.pack(B, G * H_kv, H_kv, S_q, S_kv, d, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3]),
+        jattn.BF16 if dtype == "bf16" else jattn.FP16)
+    copy = 2 * v.numel() if dtype == "bf16" and n_rt >= 4 and items * tiles >= 18 * sms else 0
+    assert (copy > 0) == (dtype == "bf16" and G == 2)
+    assert 0 <= need - copy - sms * 4 * 128 * (d + 1) * 4 < 4096
+    v *= 2.0 ** (5.0 * (torch.arange(B * H_kv, device=cuda_device).view(B, H_kv, 1, 1) % 5 - 2))
+    n = torch.tensor([S_kv, 2100], dtype=torch.int32, device=cuda_device)
+    m = torch.rand(B, S_kv, generator=torch.Generator().manual_seed(1)).to(cuda_device) < 0.9
+    allowed = m & (torch.arange(S_kv, device=cuda_device) < n[:, None])
+    v.masked_fill_(~allowed[:, None, :, None], float("nan"))
+    o, lse = jattn.fwd_diff(q, k, v, lam, INIT, kv_len=n, key_mask=m, want_lse=True)
+    rows = torch.arange(S_q, device=cuda_device)
+    whole = (items - rest) // n_rt // H_kv, (items - rest) // n_rt % H_kv * G      # where the tail begins
+    for b, h in [(0, 0), whole] + [(B - 1, G * H_kv - i) for i in (1, 2, 3, 8)]:
+        want, lref = of_rows(q, k, v, lam, b, h, rows, allowed)
+        assert near(o[b, :, h], want), (b, h)
+        assert (lse[:, b, h].double() - lref).abs().max() <= 2.0 ** -13
+    again, _ = jattn.fwd_diff(q, k, v, lam, INIT, kv_len=n, key_mask=m)
+    assert torch.equal(again, o) and jattn.device_status()[0] == jattn.OK

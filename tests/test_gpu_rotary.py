@@ -167,3 +167,38 @@ def test_other_stream_and_graph(cuda_device):
     pos += 5
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(y, jattn.rotary(q, k, pos, freqs)))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_odd_strides(cuda_device, dtype, layout, inverse):
+    """Heads an odd number of elements apart, into heads at other odd strides and
+    an odd offset: single channels at a time.  What lies between is left."""
+    B, S, H, d, rot = 2, 9, 3, 20, 12
+    g = torch.Generator().manual_seed(10)
+    x = torch.randn(B, S, H, d + 1, generator=g).to(DT[dtype]).to(cuda_device)
+    q, k = x[..., :d], x[:, :, 1:, 1:]
+    pos = torch.randint(0, 3000, (B, S), generator=g).int().to(cuda_device)
+    freqs, scale = jattn.rotary_freqs(rot, scaling="yarn", factor=8.0, device=cuda_device)
+    bufs = [torch.full((B * S * h * (d + 3) + 1,), 7.0, dtype=DT[dtype], device=cuda_device) for h in (H, H - 1)]
+    out = tuple(b[1:].view(B, S, h, d + 3)[..., :d] for b, h in zip(bufs, (H, H - 1)))
+    jattn.rotary(q, k, pos, freqs, layout=layout, scale=scale, inverse=inverse, out=out)
+    for y, x_ in zip(out, (q, k)):
+        check(y, x_, pos.cpu().numpy(), freqs.cpu().numpy(), half=layout == "half", scale=scale, inverse=inverse)
+        y.fill_(7.0)
+    assert all((b == 7.0).all() for b in bufs)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_inverse_in_16_bits(cuda_device, dtype, layout):
+    """The transposed map in every access width of the 16-bit kernels."""
+    for d, rot, parts in ((128, 128, 1), (128, 64, 2), (64, 24, 1), (36, 12, 1), (10, 6, 1)):
+        q, k = case(cuda_device, dtype, 2, 41, 3, 1, d, seed=d)
+        pos = torch.randint(0, 9000, (2, 41), generator=torch.Generator().manual_seed(11)).int()
+        freqs, scale = jattn.rotary_freqs(rot, scaling="yarn", factor=4.0, device=cuda_device)
+        kw = dict(layout=layout, parts=parts, scale=scale)
+        yq, yk = jattn.rotary(q, k, pos.to(cuda_device), freqs, inverse=True, **kw)
+        for y, x in ((yq, q), (yk, k)):
+            check(y, x, pos.numpy(), freqs.cpu().numpy(), half=layout == "half", parts=parts, scale=scale, inverse=True)
