@@ -11,7 +11,10 @@
 // and each takes its half of the channels of the same Q and K tiles, so the
 // shared-memory and L2 traffic of a key tile serves both maps.  Per key tile
 // the CTA does 2 x 128 x 128 exponentials (the dense kernel's count) for 3/4
-// of its products: the exponentials bound it.
+// of its products.  Neither unit is full (exponential unit 55% active, tensor
+// pipe 46% at 12 heads x 4736): what bounds a long walk is the softmax warps'
+// turns on the exponential unit, about 650 clocks per half and 150 for the
+// hand-over, of which the unit works 430.
 //   warps 0..3  softmax of map 0, warps 4..7 of map 1: one thread per query
 //               row, online softmax with lazy rescale, P into the S columns;
 //               then O_1 / l_1 - lambda O_2 / l_2 for half of the channels
@@ -54,7 +57,8 @@ constexpr int BN = 128;                // keys per tile
 constexpr int kMmaWarp = 8, kProducerWarp = 9, kMaskWarp = 10, kShareWarp = 11;
 constexpr int kThreads = 384;
 // Register split after setmaxnreg, together the 384 x 168 the block launches
-// with: the fewest spills (-Xptxas -v: at most 16 bytes, outside the walks).
+// with: the fewest spills (-Xptxas -v: 8 or 16 bytes of stores, 32 or 40 in three
+// of the four few-row forms).
 template <int D> __host__ __device__ constexpr uint32_t regs_softmax() { return D == 128 ? 208u : 216u; }
 template <int D> __host__ __device__ constexpr uint32_t regs_other() { return (kThreads * 168u - 256u * regs_softmax<D>()) / 128u; }
 constexpr uint32_t kTmemCols = 512;
@@ -1377,6 +1381,8 @@ DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms) {
   DiffWalk w{};
   if (items < sms) {
     // fewer items than SMs: cut them where a CTA still gets a few key tiles
+    // (every such call; what the parts' way through memory costs is not weighed
+    // against the tiles saved as it is for the last wave below)
     w.ctas = static_cast<int>(items);
     if (tiles >= 8) {
       const long long c = items * tiles / 4;
@@ -1406,9 +1412,9 @@ DiffWalk diff_walk(long long items, int n_rt, int S_kv, int sms) {
 // Whether bf16 operands get an fp16 copy of V: about 8 us and three passes over
 // V, against a fifth of the walk for P in two parts.  Several row tiles have to
 // share each V tile, and the walk to be long: 2 x 24 heads, 1000 tokens (20 key
-// tiles per SM): 75 us with the copy, 77 without; 2 x 24 x 4608: 941 and 1169;
-// 8 heads, 2000 tokens (14): 85 and 83; 24 heads, 300 x 8000 (3 row tiles):
-// 127 and 112.
+// tiles per SM): 73 us with the copy, 72 without; 2 x 24 x 4608: 833 and 1040;
+// 8 heads, 2000 tokens (14): 76 and 71; 24 heads, 300 x 8000 (3 row tiles):
+// 122 and 100.
 bool diff_widens_v(long long items, int n_rt, int S_kv, int sms) {
   return n_rt >= 4 && items * ((S_kv + BN - 1) / BN) >= 18ll * sms;
 }

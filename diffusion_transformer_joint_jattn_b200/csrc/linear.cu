@@ -969,7 +969,8 @@ LinearPlan plan_linear(int M, int N, int K, int out_dtype) {
   // 256 x 256 tiles once they nearly fill the 74 pairs (1536 x 3000 x 1360, 72
   // tiles: 17.6 us against 19.1; 1024 x 4096 x 1024, 64 tiles: 12.6 against
   // 11.8); emptying their accumulators on the way they need several rounds
-  // (2048 x 2048 x 2048 to fp32, 128 tiles: 40 us against 29)
+  // (2048 x 2048 x 2048 to fp32, 128 tiles: 24 us against 21; 4096 x 2048 x 2048,
+  // 256 tiles: 43 against 39)
   if (pair_tiles >= (pl.flush ? 296 : 68)) {
     pl.pair = true;
     pl.bn = pn;

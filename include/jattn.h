@@ -480,6 +480,9 @@ typedef struct {
  *   lse      : fp32 [2][B][H][S_q], the natural-log sum-exp of both maps
  *              (-inf for a row without a key), or NULL.
  *   o and lse overlap no input and not each other.
+ *   With bf16 operands and long prompts V is held in fp16 beside a power of two
+ *   per (batch entry, K/V head): values below 2^-29 of that head's largest
+ *   lose bits.
  *   softmax_scale <= 0 selects 1 / sqrt(d / 2).
  *   workspace: device scratch of at least jattn_fwd_diff_workspace()
  *              bytes, 256-byte aligned (NULL where that is 0).  Calls that
