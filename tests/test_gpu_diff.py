@@ -483,3 +483,29 @@ def test_whole_items_and_a_shared_tail(cuda_device, dtype, d, G, H_kv):
         assert (lse[:, b, h].double() - lref).abs().max() <= 2.0 ** -13
     again, _ = jattn.fwd_diff(q, k, v, lam, INIT, kv_len=n, key_mask=m)
     assert torch.equal(again, o) and jattn.device_status()[0] == jattn.OK
+
+
+def test_long_walks_at_once_and_captured(cuda_device):
+    """Calls whose accumulators are emptied on the way have sums of their own: two
+    captured graphs replayed at the same time, with new queries, and eager calls
+    on two streams, give the bits of one call alone."""
+    for H, H_kv, S_q, S_kv in ((1, 1, 148 * 128, 70000), (8, 8, 1, 1 << 20)):
+        q, k, v, lam = make_long(cuda_device, "bf16", H, H_kv, S_q, S_kv)
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        graphs, outs = [torch.cuda.CUDAGraph() for _ in streams], []
+        jattn.fwd_diff(q, k, v, lam, INIT)
+        torch.cuda.synchronize()
+        for g in graphs:
+            with torch.cuda.graph(g):
+                outs.append(jattn.fwd_diff(q, k, v, lam, INIT, want_lse=True))
+        q.neg_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+        eager = [jattn.fwd_diff(q, k, v, lam, INIT, want_lse=True, stream=s) for s in streams]
+        torch.cuda.synchronize()
+        want = jattn.fwd_diff(q, k, v, lam, INIT, want_lse=True)
+        assert all(torch.equal(a, b) for got in outs + eager for a, b in zip(got, want))
+    assert jattn.device_status()[0] == jattn.OK
